@@ -135,6 +135,69 @@ moe_status_t moe_route_topk_grouped(const float* logits, const float* bias, int 
                                     int n_group, int topk_group, float routed_scaling_factor,
                                     int32_t* topk_ids, float* topk_w, moe_stream_t stream);
 /*
+ * S1 with a choice of scores — the general form behind the two above, for routers whose bias
+ * steers the selection of softmax scores, whose groups are ranked by their best expert, whose
+ * weights are not renormalised, or whose logits are bf16, strided or masked.
+ *   s_e = softmax(l)_e (MOE_SCORE_SOFTMAX) or sigmoid(l_e) (MOE_SCORE_SIGMOID);
+ *   c_e = s_e + bias_e. bias (fp32 [E], finite, NULL = 0) steers the selection only. Without
+ *   a bias the experts are ranked by their logits, of which s is an increasing function.
+ *   The E experts form n_group consecutive groups. A group scores its largest c
+ *   (MOE_GROUP_MAX) or the sum of its two largest (MOE_GROUP_TOP2; its one c where it has one
+ *   live expert). The topk_group best groups are kept, ties to the lower group. The topk
+ *   largest c among their experts are chosen, ties to the lower id, in that order.
+ *   topk_w = routed_scaling_factor * s_j, divided by the sum of the chosen s if renormalize.
+ * An expert whose logit is -inf or NaN is masked: its s is 0 and it is chosen only where the
+ * kept groups have fewer than topk live experts, after those, in order of id and with weight
+ * 0, so that ids stay valid and distinct for moe_permute. A row without a live expert gets
+ * weight 0 throughout. Softmax gives +inf logits equal shares of 1. Decisions are those of
+ * 64-bit arithmetic: 32-bit scores decide only where they differ by more than their error.
+ *   logits fp32 (in_is_bf16 = 0) or bf16 (1) [T,E], rows row_stride elements apart (>= E).
+ *   topk_ids int32 / topk_w fp32 [T,topk] out, dense.
+ * E % n_group, 1 <= topk_group <= n_group, 1 <= topk <= topk_group*E/n_group and a finite
+ * positive scaling factor, else INVALID_ARG; E > 1024, n_group > 32 or topk > 32: UNSUPPORTED.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score_t;
+moe_status_t moe_route_scored(const void* logits, int in_is_bf16, int64_t row_stride, const float* bias, int T, int E,
+                              int topk, int scoring, int n_group, int topk_group, int group_score, int renormalize,
+                              float routed_scaling_factor, int32_t* topk_ids, float* topk_w, moe_stream_t stream);
+
+/*
+ * What stands before the layer — residual addition and root-mean-square norm of rows, in one
+ * pass, with the normalised rows in bf16 (for the router) and/or quantised for the experts:
+ *   r = x + residual (r = x if residual is NULL), in fp32;   residual_out = bf16(r);
+ *   y = r / sqrt(mean(r^2) + eps) * weight, in fp32 (weight NULL = 1);   y_out = bf16(y);
+ *   codes, scales = y quantised per 32 values (from fp32, not from y_out): MOE_Q_MXFP8 by the
+ *   rule of moe_quantize_mxfp8, MOE_Q_MXFP4 by that of moe_quantize_mxfp4. A block with an
+ *   infinity or NaN gets the NaN scale 255 (and e4m3 NaN or +0 e2m1 codes).
+ * x bf16 or fp32 [T,H]; residual, residual_out and y bf16 [T,H]; weight bf16 or fp32 [H];
+ * codes uint8 [T,H] (MXFP8) or [T,H/2] (MXFP4, even column in the low nibble) and scales
+ * uint8 e8m0 [T,H/32], dense; deq bf16 [T,H] or NULL, dense: the values codes and scales stand for.
+ * Strides are in elements between rows; 0 means H. residual_out, y and codes with scales are each optional;
+ * residual_out may be residual and y may be x (bf16) with equal strides; no other overlap.
+ * H % 8 (H % 32 with quant), strides % 8 and 16-byte aligned pointers (scales: any), else
+ * MOE_ERR_ALIGNMENT; eps finite and > 0, strides >= H; H > 32768: UNSUPPORTED. The sum of
+ * squares is taken in fp32: it must not overflow there.
+ */
+typedef enum { MOE_Q_NONE = 0, MOE_Q_MXFP8 = 1, MOE_Q_MXFP4 = 2 } moe_quant_t;
+typedef struct {
+    const void* x;
+    const void* residual;           /* or NULL */
+    const void* weight;             /* or NULL */
+    int32_t x_is_f32, weight_is_f32;
+    int32_t T, H;
+    int64_t x_stride, residual_stride, residual_out_stride, y_stride;
+    float eps;
+    int32_t quant;                  /* moe_quant_t */
+    void* residual_out;             /* or NULL */
+    void* y;                        /* or NULL */
+    uint8_t* codes;                 /* with quant */
+    uint8_t* scales;                /* with quant */
+    void* deq;                      /* with quant, or NULL */
+} moe_rmsnorm_args_t;
+moe_status_t moe_add_rmsnorm(const moe_rmsnorm_args_t* args, moe_stream_t stream);
+
+/*
  * S2 — permute into expert-contiguous segments (MoonEP page: module docstring
  * and MoonEPExperts.apply; cu_seqlens = cumsum of per-row lengths).
  *   topk_ids/topk_w [T,topk]; replica_src int32 [B] (source expert of each
@@ -324,6 +387,44 @@ moe_status_t moe_quantize_nvfp4(const void* in, int in_is_f32, int R, int K,
  */
 moe_status_t moe_quantize_mxfp8(const void* in, int in_is_f32, int R, int K, uint8_t* codes,
                                 uint8_t* scales, moe_stream_t stream);
+/*
+ * S2q — MXFP4 quantisation of rows by the OCP MX v1.0 rule, the 4-bit sibling of
+ * moe_quantize_mxfp8: activations for moe_grouped_gemm_mxfp4, or bf16 weights into the
+ * MOE_W_MXFP4 format (rows of [G*N, K]). Per 32 values, scale 2^e with
+ * e = floor(log2 amax) - 2 clamped to [-127, 127] (e = -127 for an all-zero block),
+ * q = e2m1_rne_satfinite(v / 2^e). A block with an infinity or NaN gets the NaN scale 255 and
+ * +0 codes (moe_prepare_weights refuses such weights).
+ *   in      bf16 (in_is_f32 = 0) or fp32 (in_is_f32 = 1) [R,K], K % 32 == 0, rows in_stride
+ *           elements apart (>= K; a multiple of 8).
+ *   codes   uint8 [R,K/2] packed e2m1 (even k in the low nibble).   scales uint8 [R,K/32] e8m0.
+ *   deq     optional bf16 [R,K]: the values they stand for (exact in bf16).
+ */
+moe_status_t moe_quantize_mxfp4(const void* in, int in_is_f32, int64_t in_stride, int R, int K, uint8_t* codes,
+                                uint8_t* scales, void* deq, moe_stream_t stream);
+
+/*
+ * S3/S5 with MXFP4 activations (W4A4) — the block-scaled grouped GEMM on 4-bit operands. For
+ * every cu_seqlens segment g and row r in it, with a row i = row_idx[r] (i = r if NULL):
+ *   out[r, n] = alpha_g * sum_k e2m1(a[i,k]) * 2^(a_scale[i,k/32] - 127)
+ *                              * e2m1(W[g][n,k]) * 2^(W_scale[g][n,k/32] - 127)
+ * with the products summed in fp32 by the tensor cores (kind::mxf4), rounded once to bf16;
+ * rows [cu_seqlens[G-1], M_alloc) of out are written as zero. A row whose row_idx lies outside
+ * [0, a_rows) counts as zeros and sets MOE_ERR_DEVICE in the error word. An activation block
+ * with the NaN scale 255 makes its row NaN.
+ *   a_codes uint8 [a_rows, K/2];  a_scales uint8 [a_rows, K/32] — the outputs of
+ *           moe_quantize_mxfp4 or moe_add_rmsnorm.
+ *   row_idx int32 [M_alloc] or NULL (a_rows >= M_alloc): the permutation's perm_token, so that
+ *           token rows quantised once are gathered by the GEMM itself.
+ *   w       MXFP4 weights prepared by moe_prepare_weights (else NOT_PREPARED); other formats:
+ *           UNSUPPORTED.
+ *   out bf16 [M_alloc, N], N % 8 == 0; cu_seqlens int32 [G] on device; G <= 1024.
+ *   ws: at least 256 bytes (the error word).
+ */
+moe_status_t moe_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int a_rows,
+                                    const int32_t* row_idx, int M_alloc, const moe_weight_t* w,
+                                    const int32_t* cu_seqlens, void* out, void* ws, size_t ws_bytes,
+                                    moe_stream_t stream);
+
 /*
  * S0 — one-time conversion of FP4 weights into the kernel's tile layout
  * (FlashInfer MoE-EP page, process_weights_after_loading; DeepSeek-V4 FI page,

@@ -29,6 +29,9 @@ STATUS = ["MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_UNSUPPORTED", "MOE_ERR_ALIGN
           "MOE_ERR_WORKSPACE_TOO_SMALL", "MOE_ERR_CUDA", "MOE_ERR_DEVICE", "MOE_ERR_TIMEOUT",
           "MOE_ERR_NOT_PREPARED"]
 ACT = {"silu": 0, "situ": 1, "swigluoai": 2}
+SCORING = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORE = {"max": 0, "top2": 1}
+QUANT = {None: 0, "mxfp8": 1, "mxfp4": 2}
 WFMT = {"bf16": 0, "mxfp4": 1, "nvfp4": 2}
 
 # Every symbol include/moe.h declares.
@@ -37,7 +40,8 @@ EXPORTS = ["moe_status_string", "moe_version", "moe_route_topk", "moe_permute_wo
            "moe_combine", "moe_quantize_nvfp4", "moe_prepared_weight_bytes", "moe_prepare_weights",
            "moe_forward_workspace_size", "moe_forward", "moe_get_device_error", "moe_permute_noalloc",
            "moe_permute_noalloc_status", "moe_grouped_gemm_nvfp4", "moe_quantize_mxfp8", "moe_route_topk_grouped",
-           "moe_bias_act_and_mul", "moe_forward_workspace_size_args"]
+           "moe_bias_act_and_mul", "moe_forward_workspace_size_args", "moe_route_scored", "moe_add_rmsnorm",
+           "moe_quantize_mxfp4", "moe_grouped_gemm_mxfp4"]
 
 
 class MoEError(RuntimeError):
@@ -64,6 +68,17 @@ class moe_act_ex_t(ctypes.Structure):
                 ("swiglu_limit", ctypes.c_float)]
 
 
+class moe_rmsnorm_args_t(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("x_is_f32", ctypes.c_int32), ("weight_is_f32", ctypes.c_int32),
+                ("T", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+                ("residual_out_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("quant", ctypes.c_int32), ("residual_out", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("deq", ctypes.c_void_p)]
+
+
 class moe_forward_args_t(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("router_logits", ctypes.c_void_p),
                 ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32),
@@ -88,7 +103,7 @@ ROUTING = {"renormalize": 0, "deepseek_v3": 1, "given": 2}
 MOE_FWD_STAGE_EVENTS = 7
 
 
-_P, _I, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_P, _I, _S, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
 _sig = {
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_version": (ctypes.c_char_p, []),
@@ -112,6 +127,10 @@ _sig = {
     "moe_route_topk_grouped": (_I, [_P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P]),
     "moe_bias_act_and_mul": (_I, [_P, _P, _I, _P, _P, _P, _I, _P, _I, _I, ctypes.POINTER(moe_act_ex_t), _P, _P]),
     "moe_forward_workspace_size_args": (_S, [ctypes.POINTER(moe_forward_args_t)]),
+    "moe_route_scored": (_I, [_P, _I, _L, _P, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P]),
+    "moe_add_rmsnorm": (_I, [ctypes.POINTER(moe_rmsnorm_args_t), _P]),
+    "moe_quantize_mxfp4": (_I, [_P, _I, _L, _I, _I, _P, _P, _P, _P]),
+    "moe_grouped_gemm_mxfp4": (_I, [_P, _P, _I, _P, _I, ctypes.POINTER(moe_weight_t), _P, _P, _P, _S, _P]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -134,6 +153,30 @@ def _stream(stream=None) -> int:
 def _check(status: int, where: str) -> None:
     if status != MOE_OK:
         raise MoEError(status, where)
+
+
+def _launch_stream(dev: torch.device, stream) -> int:
+    """The stream of a call on `dev`'s tensors; the kernels run on the current device."""
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"need tensors on the current CUDA device, got {dev}")
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+
+
+def _want(t, name: str, shape, dtype, dev: torch.device, dense: bool = True) -> None:
+    """A tensor argument of this shape and type on this device; rows contiguous, and dense unless
+    the call takes a row stride."""
+    if t.shape != shape or t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)) or t.device != dev:
+        raise ValueError(f"{name}: need {tuple(shape)} {dtype} on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    if dense:
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: need a contiguous tensor, got strides {t.stride()}")
+    elif t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: need contiguous rows that do not overlap, got strides {t.stride()}")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements between rows (a single row's stride is not used)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def version() -> str:
@@ -221,6 +264,78 @@ def moe_route_topk_grouped(logits: torch.Tensor, topk: int, n_group: int, topk_g
     return ids, w
 
 
+def moe_route_scored(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias=None, n_group: int = 1,
+                     topk_group: int = 1, group_score: str = "max", renormalize: bool = True,
+                     routed_scaling_factor: float = 1.0, ids=None, w=None, stream=None):
+    """Routing by softmax or sigmoid scores, with a selection bias (fp32 [E]), groups kept by their
+    best ("max") or two best ("top2") experts, and raw or renormalised weights. logits fp32 or bf16
+    [T,E], rows in any stride; a logit of -inf masks its expert."""
+    T, E = logits.shape
+    dev = logits.device
+    st = _launch_stream(dev, stream)
+    _want(logits, "logits", (T, E), (torch.float32, torch.bfloat16), dev, dense=False)
+    if bias is not None:
+        _want(bias, "bias", (E,), torch.float32, dev)
+    if ids is None:
+        ids = torch.empty(T, topk, dtype=torch.int32, device=dev)
+    else:
+        _want(ids, "ids", (T, topk), torch.int32, dev)
+    if w is None:
+        w = torch.empty(T, topk, dtype=torch.float32, device=dev)
+    else:
+        _want(w, "w", (T, topk), torch.float32, dev)
+    _check(_lib.moe_route_scored(_ptr(logits), logits.dtype == torch.bfloat16, _row_stride(logits), _ptr(bias), T, E,
+                                 topk, SCORING[scoring], n_group, topk_group, GROUP_SCORE[group_score], renormalize,
+                                 routed_scaling_factor, _ptr(ids), _ptr(w), st), "moe_route_scored")
+    return ids, w
+
+
+def moe_add_rmsnorm(x: torch.Tensor, weight=None, residual=None, eps: float = 1e-6, quant: str | None = None,
+                    want_y: bool = True, deq: bool = False, out=None, stream=None):
+    """r = x + residual; y = r / sqrt(mean(r^2) + eps) * weight; y optionally quantised to "mxfp8" or
+    "mxfp4" rows. x bf16 or fp32 [T,H], residual bf16 [T,H], weight bf16 or fp32 [H] (rows of x and
+    residual in any stride).
+    ``out``: optional dict of caller-allocated outputs (any of residual, y, codes, scales, deq; the
+    rows of residual and y may be strided, residual may be the input's own tensor); the others are
+    allocated here. Returns a dict with those five, None where not asked for: ``residual`` (bf16
+    rows of r) comes with a residual, ``y`` (bf16) with want_y, ``codes`` and ``scales`` with quant,
+    ``deq`` (bf16, the values they stand for) with deq."""
+    T, H = x.shape
+    dev = x.device
+    st = _launch_stream(dev, stream)
+    out = out or {}
+    bf16 = torch.bfloat16
+    _want(x, "x", (T, H), (torch.float32, bf16), dev, dense=False)
+    if residual is not None:
+        _want(residual, "residual", (T, H), bf16, dev, dense=False)
+    if weight is not None:
+        _want(weight, "weight", (H,), (torch.float32, bf16), dev)
+    if deq and quant is None:
+        raise ValueError("deq needs quant")
+
+    def buf(name, wanted, shape, dtype, dense=True):
+        if not wanted:
+            return None
+        t = out.get(name)
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        _want(t, name, shape, dtype, dev, dense)
+        return t
+
+    r = buf("residual", residual is not None, (T, H), bf16, dense=False)
+    y = buf("y", want_y, (T, H), bf16, dense=False)
+    codes = buf("codes", quant is not None, (T, H // 2 if quant == "mxfp4" else H), torch.uint8)
+    scales = buf("scales", quant is not None, (T, H // 32), torch.uint8)
+    d = buf("deq", deq, (T, H), bf16)
+    a = moe_rmsnorm_args_t(_ptr(x), _ptr(residual), _ptr(weight), x.dtype != bf16,
+                           weight is not None and weight.dtype != bf16, T, H, _row_stride(x),
+                           0 if residual is None else _row_stride(residual), 0 if r is None else _row_stride(r),
+                           0 if y is None else _row_stride(y), eps, QUANT[quant], _ptr(r), _ptr(y), _ptr(codes),
+                           _ptr(scales), _ptr(d))
+    _check(_lib.moe_add_rmsnorm(ctypes.byref(a), st), "moe_add_rmsnorm")
+    return dict(residual=r, y=y, codes=codes, scales=scales, deq=d)
+
+
 def permute_workspace(T: int, topk: int, E: int, B: int, device="cuda") -> torch.Tensor:
     n = _lib.moe_permute_workspace_size(T, topk, E, B)
     return torch.zeros(n, dtype=torch.uint8, device=device)
@@ -280,6 +395,32 @@ def moe_grouped_gemm_nvfp4(a_codes: torch.Tensor, a_sb: torch.Tensor, a_s: torch
     _check(_lib.moe_grouped_gemm_nvfp4(_ptr(a_codes), _ptr(a_sb), _ptr(a_s), M, ctypes.byref(w.desc),
                                        _ptr(cu_seqlens), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
            "moe_grouped_gemm_nvfp4")
+    return out
+
+
+def moe_grouped_gemm_mxfp4(a_codes: torch.Tensor, a_scales: torch.Tensor, w: Weight, cu_seqlens: torch.Tensor,
+                           row_idx=None, out=None, ws=None, stream=None) -> torch.Tensor:
+    """Block-scaled grouped GEMM on MXFP4 activations (codes [R,K/2], e8m0 scales [R,K/32]) and
+    prepared MXFP4 weights. row_idx (int32 [M]): row r of the segments is row row_idx[r] of a (the
+    permutation's perm_token); without it the R rows are in segment order. bf16 out [M,N]."""
+    R, dev = a_codes.shape[0], a_codes.device
+    st = _launch_stream(dev, stream)
+    u8 = torch.uint8
+    _want(a_codes, "a_codes", (R, w.K // 2), u8, dev)
+    _want(a_scales, "a_scales", (R, w.K // 32), u8, dev)
+    _want(cu_seqlens, "cu_seqlens", (w.G,), torch.int32, dev)
+    M = R
+    if row_idx is not None:
+        M = row_idx.shape[0]
+        _want(row_idx, "row_idx", (M,), torch.int32, dev)
+    if out is None:
+        out = torch.empty(M, w.N, dtype=torch.bfloat16, device=dev)
+    else:
+        _want(out, "out", (M, w.N), torch.bfloat16, dev)
+    if ws is None:
+        ws = torch.zeros(256, dtype=u8, device=dev)
+    _check(_lib.moe_grouped_gemm_mxfp4(_ptr(a_codes), _ptr(a_scales), R, _ptr(row_idx), M, ctypes.byref(w.desc),
+                                       _ptr(cu_seqlens), _ptr(out), _ptr(ws), ws.numel(), st), "moe_grouped_gemm_mxfp4")
     return out
 
 
@@ -348,6 +489,31 @@ def moe_quantize_mxfp8(x: torch.Tensor, stream=None):
     _check(_lib.moe_quantize_mxfp8(_ptr(x), 1 if x.dtype == torch.float32 else 0, R, K, _ptr(codes), _ptr(scales),
                                    _stream(stream)), "moe_quantize_mxfp8")
     return codes, scales
+
+
+def moe_quantize_mxfp4(x: torch.Tensor, deq: bool = False, out=None, stream=None):
+    """MXFP4 quantisation of rows (bf16 or fp32 [R,K], in any row stride): packed e2m1 codes [R,K/2],
+    e8m0 scales [R,K/32] and, with deq, the bf16 values they stand for [R,K] (else None). ``out``:
+    optional dict of caller-allocated outputs (any of codes, scales, deq)."""
+    R, K = x.shape
+    dev = x.device
+    st = _launch_stream(dev, stream)
+    out = out or {}
+    _want(x, "x", (R, K), (torch.float32, torch.bfloat16), dev, dense=False)
+
+    def buf(name, shape, dtype):
+        t = out.get(name)
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        _want(t, name, shape, dtype, dev)
+        return t
+
+    codes = buf("codes", (R, K // 2), torch.uint8)
+    scales = buf("scales", (R, K // 32), torch.uint8)
+    d = buf("deq", (R, K), torch.bfloat16) if deq else None
+    _check(_lib.moe_quantize_mxfp4(_ptr(x), x.dtype == torch.float32, _row_stride(x), R, K, _ptr(codes), _ptr(scales),
+                                   _ptr(d), st), "moe_quantize_mxfp4")
+    return codes, scales, d
 
 
 def forward_workspace(T_max, H, I, E, B, topk, wfmt="bf16", act_quant=0, device="cuda") -> torch.Tensor:

@@ -221,6 +221,72 @@ moe_status_t moe_route_topk_grouped(const float* logits, const float* bias, int 
                                             topk_ids, topk_w, S(stream), false));
 }
 
+moe_status_t moe_route_scored(const void* logits, int in_is_bf16, int64_t row_stride, const float* bias, int T, int E,
+                              int topk, int scoring, int n_group, int topk_group, int group_score, int renormalize,
+                              float routed_scaling_factor, int32_t* topk_ids, float* topk_w, moe_stream_t stream) {
+    if (T < 0 || E < 1 || topk < 1 || n_group < 1 || topk_group < 1 || topk_group > n_group) return MOE_ERR_INVALID_ARG;
+    if (E % n_group || topk > (long long)topk_group * (E / n_group) || row_stride < E) return MOE_ERR_INVALID_ARG;
+    if (scoring != MOE_SCORE_SOFTMAX && scoring != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+    if (group_score != MOE_GROUP_MAX && group_score != MOE_GROUP_TOP2) return MOE_ERR_INVALID_ARG;
+    if (!std::isfinite(routed_scaling_factor) || !(routed_scaling_factor > 0.0f)) return MOE_ERR_INVALID_ARG;
+    if (E > kMaxExperts || n_group > 32 || topk > kMaxTopk) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!logits || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
+    const RouteScored r{logits, in_is_bf16 != 0, row_stride, bias,        T,
+                        E,      topk,            scoring,    n_group,     topk_group,
+                        group_score, renormalize != 0, routed_scaling_factor, topk_ids, topk_w};
+    return cuda_status(launch_route_scored(r, S(stream), false));
+}
+
+moe_status_t moe_add_rmsnorm(const moe_rmsnorm_args_t* p, moe_stream_t stream) {
+    if (!p || p->T < 0 || p->H < 1) return MOE_ERR_INVALID_ARG;
+    if (p->quant < MOE_Q_NONE || p->quant > MOE_Q_MXFP4) return MOE_ERR_INVALID_ARG;
+    if (!std::isfinite(p->eps) || !(p->eps > 0.0f)) return MOE_ERR_INVALID_ARG;
+    if (p->H > 32768) return MOE_ERR_UNSUPPORTED;
+    moe_rmsnorm_args_t a = *p;
+    for (int64_t* s : {&a.x_stride, &a.residual_stride, &a.residual_out_stride, &a.y_stride}) {
+        if (*s == 0) *s = a.H;
+        if (*s < a.H) return MOE_ERR_INVALID_ARG;
+        if (*s % 8) return MOE_ERR_ALIGNMENT;
+    }
+    if (a.H % (a.quant == MOE_Q_NONE ? 8 : 32)) return MOE_ERR_ALIGNMENT;
+    if (a.T == 0) return MOE_OK;
+    if (!a.x || (!a.residual_out && !a.y && a.quant == MOE_Q_NONE)) return MOE_ERR_INVALID_ARG;
+    if (a.quant != MOE_Q_NONE ? !a.codes || !a.scales : a.codes || a.scales || a.deq) return MOE_ERR_INVALID_ARG;
+    for (const void* q : {a.x, a.residual, a.weight, (const void*)a.residual_out, (const void*)a.y, (const void*)a.codes,
+                          (const void*)a.deq})
+        if (!aligned16(q)) return MOE_ERR_ALIGNMENT;
+    return cuda_status(launch_add_rmsnorm(a, S(stream), false));
+}
+
+moe_status_t moe_quantize_mxfp4(const void* in, int in_is_f32, int64_t in_stride, int R, int K, uint8_t* codes,
+                                uint8_t* scales, void* deq, moe_stream_t stream) {
+    if (R < 0 || K < 0 || in_stride < K) return MOE_ERR_INVALID_ARG;
+    if (K % 32 || in_stride % 8) return MOE_ERR_ALIGNMENT;
+    if ((size_t)R * K == 0) return MOE_OK;
+    if (!in || !codes || !scales) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(in) || !aligned16(codes) || (deq && !aligned16(deq))) return MOE_ERR_ALIGNMENT;
+    return cuda_status(launch_quant_mxfp4(in, in_is_f32 != 0, in_stride, R, K, codes, scales, deq, S(stream), false));
+}
+
+moe_status_t moe_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int a_rows, const int32_t* row_idx,
+                                    int M_alloc, const moe_weight_t* w, const int32_t* cu_seqlens, void* out, void* ws,
+                                    size_t ws_bytes, moe_stream_t stream) {
+    if (!w || M_alloc < 0 || a_rows < 0 || w->G < 1 || w->N < 1 || w->K < 1) return MOE_ERR_INVALID_ARG;
+    if (w->G > 1024) return MOE_ERR_UNSUPPORTED;
+    if (w->fmt != MOE_W_MXFP4) return MOE_ERR_UNSUPPORTED;
+    moe_status_t s = check_weight(*w, w->G, w->N, w->K);
+    if (s != MOE_OK) return s;
+    if (M_alloc == 0) return MOE_OK;
+    if (a_rows < 1 || (!row_idx && a_rows < M_alloc)) return MOE_ERR_INVALID_ARG;
+    if (!a_codes || !a_scales || !cu_seqlens || !out || !ws) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(a_codes) || !aligned16(out) || w->N % 8) return MOE_ERR_ALIGNMENT;
+    if (ws_bytes < kErrBytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    const Mxf4Problem p{a_codes,   a_scales,  a_rows,          row_idx,    M_alloc, w->G, w->N, w->K,
+                        w->kdata,  w->kscale, weight_alpha(*w), cu_seqlens, out,     reinterpret_cast<DevError*>(ws)};
+    return cuda_status(launch_gemm_mxf4(p, S(stream), false));
+}
+
 size_t moe_permute_workspace_size(int T, int topk, int E, int B) {
     if (T < 0 || topk < 1 || E < 1 || B < 0) return 0;
     return kErrBytes + permute_ws_layout(T, topk, E, B).bytes;

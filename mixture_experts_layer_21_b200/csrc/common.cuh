@@ -104,6 +104,15 @@ MOE_DEV void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, 
         "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
+// Four rows y0..y3 of a 2-D map whose box is one row high, one after the other in shared memory;
+// a row past the map's last reads as zero.
+MOE_DEV void tma_gather4(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y0, int y1, int y2, int y3) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(smem_u32(bar))
+        : "memory");
+}
 // The same two loads with an L2 cache policy (a createpolicy value; see l2_policy).
 MOE_DEV void tma_load_2d_hint(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, uint64_t pol) {
     asm volatile(
@@ -280,6 +289,25 @@ MOE_DEV void mma_mx8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint3
 __host__ __device__ constexpr uint32_t idesc_mx8(int M, int N, uint32_t id) {
     return (id << 4) | (5u << 7) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) |
            (id << 29);
+}
+// The same with e8m0 scales, one per 32 K values (kind::mxf4): K = 64 per instruction takes two
+// scales per row, the byte pair `id` (0 or 2) of the 32-bit TMEM word at sfa / sfb; the id goes
+// in the descriptor and in bits 30-31 of both scale addresses.
+MOE_DEV void mma_mxf4_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+}
+// Its instruction descriptor: B scale id at [4,6), A and B e2m1 (1) at [7,10) and [10,13),
+// N >> 3 at [17,23), scale format 1 = ue8m0 at bit 23, M >> 4 at [24,29), A scale id at [29,31).
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, uint32_t id) {
+    return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(M >> 4) << 24) | (id << 29);
 }
 // Copies 32 rows x 16 bytes of shared memory (rows 16 bytes apart) into tensor-memory
 // lanes 0..31, columns taddr..taddr+3 (bytes 4c..4c+3 of a row in column c), and the

@@ -39,23 +39,10 @@
 // MOE_ERR_TIMEOUT in the error word, stops all roles, lets copies in flight land,
 // frees TMEM and returns.
 #include <cmath>
-#include <mutex>
 
-#include "internal.h"
+#include "gemm_common.cuh"
 
 namespace moe {
-
-constexpr int kMaxG = 1024;      // segment table capacity (weight rows)
-constexpr int kMaxStages = 16;
-constexpr int kCtrlBytes = 12288;
-constexpr int kSmemLimit = 232448;
-constexpr int kSmemBudget = kSmemLimit - 1024 - kCtrlBytes;
-
-__host__ __device__ constexpr int round1024(int b) { return (b + 1023) & ~1023; }
-__host__ __device__ constexpr int cmin(int a, int b) { return a < b ? a : b; }
-__host__ __device__ constexpr int tmem_cols_pow2(int c) {
-    return c <= 32 ? 32 : c <= 64 ? 64 : c <= 128 ? 128 : c <= 256 ? 256 : 512;
-}
 
 struct GemmArgs {
     const int32_t* cu;
@@ -89,97 +76,6 @@ struct GemmArgs {
     const __nv_bfloat16* gx;
     int gather_rows;
 };
-
-struct CtrlBlock {
-    uint64_t full[kMaxStages], empty[kMaxStages];          // operand ring (smem or TMEM)
-    uint64_t raw_full[kMaxStages], raw_empty[kMaxStages];  // raw ring (FP4)
-    uint64_t tfull[2], tempty[2], drain[6];
-    uint32_t tmem_slot;
-    int abort;
-    int cu[kMaxG];
-    int tpre[kMaxG + 1];
-};
-static_assert(sizeof(CtrlBlock) <= kCtrlBytes, "control block");
-
-// ------------------------------------------------------------------ shared pieces
-
-template <int BT>
-__device__ __forceinline__ void decode_tile(int L, const CtrlBlock* c, int G, int NT, int& g, int& nt,
-                                            int& row0, int& rows) {
-    int lo = 0, hi = G - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (c->tpre[mid] <= L) lo = mid;
-        else hi = mid - 1;
-    }
-    g = lo;
-    const int mcount = (c->tpre[g + 1] - c->tpre[g]) / NT;
-    const int r = L - c->tpre[g];
-    nt = r / mcount;
-    const int mt = r - nt * mcount;
-    const int start = g ? c->cu[g - 1] : 0;
-    // the segment's mcount = ceil(len / BT) token tiles share its rows evenly (in multiples of
-    // 16, at most BT each), so that the tiles of one weight block take about the same time and
-    // read the weight tile from L2 together; (mcount - 1) * rs < len keeps every tile non-empty
-    const int len = c->cu[g] - start;
-    const int rs = min(BT, ((len + mcount - 1) / mcount + 15) & ~15);
-    row0 = start + mt * rs;
-    rows = min(rs, c->cu[g] - row0);
-}
-
-// One warp: the segment table (cu, clamped, and the running tile count tpre).
-// Ends are clamped to [0, M_alloc] and a segment whose end lies before the previous
-// end counts as empty, so no tile can touch rows outside the buffers.
-template <int BT>
-__device__ __forceinline__ void build_segment_table(const GemmArgs& a, CtrlBlock* ctl, int lane) {
-    const int G = a.G, NT = a.NT;
-    int carry = 0, prev_chunk_end = 0;
-    for (int base = 0; base < G; base += 32) {
-        const int g = base + lane;
-        const int raw = g < G ? a.cu[g] : 0;
-        const int end = min(max(raw, 0), a.M_alloc);
-        int prev = __shfl_up_sync(0xffffffffu, end, 1);
-        if (lane == 0) prev = prev_chunk_end;
-        if (g < G && (raw != end || end < prev)) report_error(a.err, MOE_ERR_DEVICE, 1000000 + g);
-        const int len = g < G ? max(0, end - prev) : 0;
-        const int tiles = ((len + BT - 1) / BT) * NT;
-        int incl = tiles;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int n = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += n;
-        }
-        if (g < G) {
-            ctl->cu[g] = len > 0 ? end : prev;
-            ctl->tpre[g + 1] = carry + incl;
-        }
-        carry += __shfl_sync(0xffffffffu, incl, 31);
-        const int eff = g < G ? (len > 0 ? end : prev) : prev;
-        prev_chunk_end = __shfl_sync(0xffffffffu, eff, 31);
-    }
-    if (lane == 0) ctl->tpre[0] = 0;
-}
-
-// What one thread has in flight: the producer's stages (and the parity of each one's last
-// issue), or whether a tcgen05 issuer (MMA or scale copies) issued anything.
-struct Issued {
-    uint32_t mask = 0, par = 0;
-    bool tc = false;
-};
-
-// After an abort, before the CTA's shared and tensor memory are released: the producer
-// waits for its copies to land, a tcgen05 issuer commits to its own drain barrier and waits
-// for it. An abort can come after a role left its loop normally, so this runs for every
-// role once all have stopped. These waits take the default limit; nothing aborts them.
-__device__ __forceinline__ void drain_in_flight(const Issued& is, uint64_t* full, int stages, uint64_t* drain) {
-    int never = 0;
-    for (int q = 0; q < stages; ++q)
-        if (is.mask >> q & 1u) mbar_wait(&full[q], is.par >> q & 1u, &never);
-    if (is.tc && drain) {
-        mma_commit(drain);
-        mbar_wait(drain, 0, &never);
-    }
-}
 
 // Epilogue of one tile for the warp owning TMEM lanes [32q, 32q+32). The accumulator
 // buffer at column tb holds NPART partial sums per matrix. Partial j of matrix m sits at
@@ -1889,24 +1785,6 @@ __global__ void __launch_bounds__(Mx8Cfg<BT, DUAL || WIDE, TWO>::THREADS, 1)
 
 namespace {
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
 // 2-D map over a row-major [rows, cols] matrix of 16-bit elements; box = 64 cols x box_rows.
 bool make_map_2d(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, uint64_t cols,
                  uint64_t rows, uint32_t box_rows) {
@@ -1951,21 +1829,6 @@ bool make_map_3d(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, uint64
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 2-D map over rows of bytes: [rows, cols] with rows `stride` bytes apart; box = box_cols
-// bytes x box_rows. Rows and columns past the ends read as zero.
-bool make_map_u8(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t stride,
-                 uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle sw) {
-    EncodeTiledFn enc = get_encode();
-    if (!enc) return false;
-    const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {stride};
-    const cuuint32_t box[2] = {box_cols, box_rows};
-    const cuuint32_t es[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // 3-D map over MXFP4 codes [G, N, Kp/2] (packed, 4-bit elements); box = 128 values x
 // 128 rows x 1, each 16 values landing in 16 bytes of shared memory (8 bytes of codes,
 // then 8 unused) with the 128-byte swizzle. Kp % 128 == 0; rows past N read as zero.
@@ -1979,22 +1842,6 @@ bool make_map_w_u4(CUtensorMap* m, const void* ptr, uint64_t Kp, uint64_t N, uin
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, const_cast<void*>(ptr), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// `done` belongs to the caller's instantiation: kernels of one signature share a
-// function-pointer type, so the flag cannot live in a template on that type.
-template <typename Kern>
-cudaError_t set_smem_once(Kern kern, int bytes, int (&done)[64]) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!done[dev]) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-        done[dev] = 1;
-    }
-    return cudaSuccess;
 }
 
 int grid_for(const GemmProblem& p, const GemmArgs& args, int bt) {

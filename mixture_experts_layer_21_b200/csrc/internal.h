@@ -38,6 +38,20 @@ constexpr int kMaxTopk = 32;
 cudaError_t launch_route_topk(const float* logits, int T, int E, int topk, int32_t* ids, float* w,
                               cudaStream_t st, bool pdl);
 
+// The general routing; arguments as in moe_route_scored, validated, T >= 1.
+struct RouteScored {
+    const void* logits;
+    bool bf16;
+    long long stride;
+    const float* bias;
+    int T, E, topk, scoring, n_group, topk_group, group_score;
+    bool renorm;
+    float scale;
+    int32_t* ids;
+    float* w;
+};
+cudaError_t launch_route_scored(const RouteScored& r, cudaStream_t st, bool pdl);
+
 struct PermuteWs {
     int nblk;
     size_t blkcnt, blkoff, total, nrep, rep_ptr, rep_rows, rowstart, bytes;
@@ -103,6 +117,13 @@ cudaError_t launch_quant_nvfp4(const void* in, bool in_f32, int R, int K, uint8_
                                uint8_t* sb, int sb_stride, float* s, __half* deq, cudaStream_t st, bool pdl,
                                const int32_t* row_idx = nullptr, int in_rows = 0);
 
+// Rows -> MXFP4 (K % 32 == 0; rows `stride` elements apart), with the values they stand for in
+// bf16 if deq; R, K >= 1. And the residual addition with RMS norm (validated arguments, T >= 1,
+// strides filled in).
+cudaError_t launch_quant_mxfp4(const void* in, bool in_f32, long long stride, int R, int K, uint8_t* codes,
+                               uint8_t* scales, void* deq, cudaStream_t st, bool pdl);
+cudaError_t launch_add_rmsnorm(const moe_rmsnorm_args_t& a, cudaStream_t st, bool pdl);
+
 // ---------------------------------------------------------------- grouped GEMM
 // Output kinds of the GEMM epilogue.
 // OUT_MX8: the activation rows as the MXFP4 GEMM's operand records (see kMx8StageK below):
@@ -165,6 +186,21 @@ struct GemmProblem {
 };
 cudaError_t launch_grouped_gemm(const GemmProblem& p, cudaStream_t st, bool pdl);
 bool gemm_can_gather(const GemmProblem& p);
+// MXFP4 activations x MXFP4 weights; arguments as in moe_grouped_gemm_mxfp4, validated.
+struct Mxf4Problem {
+    const uint8_t* a_codes;
+    const uint8_t* a_scales;
+    int a_rows;
+    const int32_t* row_idx;
+    int M_alloc, G, N, K;
+    const void* kdata;
+    const void* kscale;
+    const float* alpha;
+    const int32_t* cu_seqlens;
+    void* out;
+    DevError* err;
+};
+cudaError_t launch_gemm_mxf4(const Mxf4Problem& p, cudaStream_t st, bool pdl);
 int choose_token_tile(long long NvS, int G, bool wide_ok);
 
 // FP4 kernel layout: tiles of 128 weight rows x 64 K values.

@@ -246,6 +246,51 @@ def route(cfg, logits, bias=None):
     return route_topk(logits, cfg.topk)
 
 
+def route_scored(logits, topk: int, scoring: str = "softmax", bias=None, n_group: int = 1, topk_group: int = 1,
+                 group_score: str = "max", renormalize: bool = True, routed_scaling_factor: float = 1.0):
+    """Routing by scores, token by token in fp64.
+
+      s = softmax(l) or sigmoid(l), 0 for a masked expert (logit -inf or NaN); c = s + bias.
+      Live experts rank by c (without a bias, by their logits), then by id; masked ones follow by id.
+      A group scores the largest c of its live experts, or the sum of up to two largest ("top2");
+      one without a live expert scores -inf. The topk_group best groups are kept (ties to the lower
+      group), and the first topk of their experts are chosen.
+      w = routed_scaling_factor * s (/ the sum of the chosen s; 0 if that is 0).
+
+    Returns ``ids [T,k] int32`` (in selection order) and ``w [T,k]`` fp64.
+    """
+    L = np.asarray(logits, dtype=np.float64)
+    T, E = L.shape
+    gs = E // n_group
+    b = np.zeros(E) if bias is None else np.asarray(bias, dtype=np.float64)
+    ids, w = np.zeros((T, topk), np.int32), np.zeros((T, topk))
+    for t in range(T):
+        l = np.where(np.isnan(L[t]), -np.inf, L[t])
+        live = l > -np.inf
+        if scoring == "sigmoid":
+            with np.errstate(over="ignore"):
+                s = 1.0 / (1.0 + np.exp(-l))         # 0 where masked
+        else:
+            with np.errstate(invalid="ignore"):      # +inf logits share the weight equally
+                z = np.where(l == l.max(), 1.0, np.exp(l - l.max()))
+            s = np.where(live, z / z.sum(), 0.0) if live.any() else np.zeros(E)
+        c = np.where(live, s + b, -np.inf)
+        key = l if bias is None else c
+        gkey = key if bias is None and group_score == "max" else c
+        score = np.full(n_group, -np.inf)
+        for g in range(n_group):
+            v = np.sort(gkey[g * gs:(g + 1) * gs])[::-1]
+            v = v[v > -np.inf][:2 if group_score == "top2" else 1]
+            score[g] = v.sum() if v.size else -np.inf
+        kept = np.lexsort((np.arange(n_group), -score))[:topk_group]
+        pick = np.flatnonzero(np.isin(np.arange(E) // gs, kept))
+        ids[t] = pick[np.lexsort((pick, -key[pick]))][:topk]
+        w[t] = s[ids[t]]
+        if renormalize:
+            w[t] = w[t] / w[t].sum() if w[t].sum() > 0 else 0.0
+    return ids, routed_scaling_factor * w
+
+
 # --------------------------------------------------------------------------------------
 # S2 permutation into expert-contiguous segments
 # --------------------------------------------------------------------------------------
@@ -475,6 +520,48 @@ def mxfp8_quantize_rows(v):
 def mxfp8_dequantize_rows(codes, scales):
     """Value of MXFP8 rows: e4m3(q) * 2^(s - 127), fp64 (exact)."""
     return e4m3_decode(codes) * np.repeat(e8m0_decode(scales), 32, axis=1)
+
+
+E2M1_EMAX = 2   # exponent of e2m1's largest normal value, 6 = 1.5 * 2^2
+
+
+def mx_scale_exponent(amax, emax: int):
+    """floor(log2 amax) - emax clamped to e8m0's [-127, 127]; -127 for a zero block."""
+    _, ex = np.frexp(np.asarray(amax, dtype=np.float64))
+    return np.where(amax > 0, np.clip(ex - 1 - emax, -127, 127), -127).astype(np.int64)
+
+
+def mxfp4_quantize_rows(v):
+    """MXFP4 quantisation of rows by the OCP MX v1.0 rule: per 32 values 2^e with
+    e = floor(log2 amax) - 2, q = e2m1_rne_satfinite(v / 2^e); signs are kept, also of zeros. A
+    block with an infinity or NaN gets scale 255 and +0 codes.
+    Returns ``codes [R,K] uint8`` (one e2m1 code each) and ``scales [R,K/32] uint8`` (e8m0)."""
+    x = np.asarray(v, dtype=np.float32).astype(np.float64)
+    R, K = x.shape
+    if K % 32:
+        raise ValueError("K must be a multiple of 32")
+    blocks = x.reshape(R, K // 32, 32)
+    bad = ~np.isfinite(blocks).all(axis=2)
+    fine = np.where(bad[:, :, None], 0.0, blocks)
+    e = mx_scale_exponent(np.abs(fine).max(axis=2), E2M1_EMAX)
+    y = fine / np.ldexp(1.0, e)[:, :, None]
+    codes = np.where(bad[:, :, None], 0, e2m1_encode(y)).astype(np.uint8)
+    return codes.reshape(R, K), np.where(bad, 255, e + 127).astype(np.uint8)
+
+
+def mxfp4_dequantize_rows(codes, scales):
+    """Value of MXFP4 rows: e2m1(q) * 2^(s - 127), fp64 (exact); NaN where the scale is 255."""
+    s = np.repeat(np.asarray(scales), 32, axis=1)
+    return np.where(s == 255, np.nan, e2m1_decode(codes) * e8m0_decode(np.where(s == 255, 127, s)))
+
+
+def add_rmsnorm(x, residual=None, weight=None, eps: float = 1e-6):
+    """r = x + residual and y = r / sqrt(mean(r^2) + eps) * weight, fp64; returns (r, y)."""
+    r = np.asarray(x, dtype=np.float64)
+    if residual is not None:
+        r = r + np.asarray(residual, dtype=np.float64)
+    y = r / np.sqrt((r * r).mean(axis=1, keepdims=True) + eps)
+    return r, y if weight is None else y * np.asarray(weight, dtype=np.float64)
 
 
 # --------------------------------------------------------------------------------------

@@ -1,0 +1,181 @@
+"""Routing by scores (moe_route_scored): ids bit-exact and weights against the 64-bit oracle, and
+the calls it refuses.
+
+Weight tolerance, relative: scores of 32 bits carry the rounding of the exponential's argument
+(half a step of |l - max| or |l|, that is |l| 2^-24 relative to the exponential), the exponential's
+2 units (2^-22), a sum of at most 1024 positive terms whose longest chain is 32 + 5 additions
+(37 * 2^-24) and three more roundings: (D + 44) 2^-24 with D the largest |l - max| or |l| of a row's
+chosen experts; twice that where the chosen scores are summed and divided again.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_21_b200 as m
+from oracle import moe_oracle as O
+
+L = m.lib()
+INVALID, UNSUP = 1, 2
+
+
+def _call(**kw):
+    d = dict(logits=16, bf16=0, stride=None, bias=None, T=4, E=16, topk=2, scoring=0, ng=1, tg=1, gs=0, renorm=1,
+             scale=1.0, ids=16, w=16)
+    d.update(kw)
+    return L.moe_route_scored(d["logits"], d["bf16"], d["E"] if d["stride"] is None else d["stride"], d["bias"], d["T"],
+                              d["E"], d["topk"], d["scoring"], d["ng"], d["tg"], d["gs"], d["renorm"], d["scale"],
+                              d["ids"], d["w"], None)
+
+
+@pytest.mark.parametrize("kw", [dict(T=-1), dict(E=0), dict(topk=0), dict(topk=17), dict(stride=15), dict(stride=0),
+                                dict(stride=-16), dict(scoring=2), dict(scoring=-1), dict(ng=0), dict(ng=3),
+                                dict(ng=4, tg=0), dict(ng=4, tg=5), dict(ng=8, tg=1, topk=3), dict(gs=2),
+                                dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf")),
+                                dict(logits=None), dict(ids=None), dict(w=None)])
+def test_refuses_bad_arguments(kw):
+    assert _call(**kw) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(E=1025), dict(E=66, ng=33, tg=33), dict(E=64, topk=33)])
+def test_refuses_unsupported_sizes(kw):
+    assert _call(**kw) == UNSUP
+
+
+def test_no_tokens_is_a_no_op():
+    assert _call(T=0, logits=None, ids=None, w=None) == 0
+
+
+@pytest.mark.parametrize("bad", ["dtype", "cpu", "bias", "cols"])
+def test_binding_refuses(bad):
+    x = torch.zeros(4, 8)
+    with pytest.raises((ValueError, RuntimeError, AssertionError)):
+        m.moe_route_scored(x.half() if bad == "dtype" else x, 2, bias=torch.zeros(7) if bad == "bias" else None)
+
+
+def test_oracle_agrees_with_the_two_special_forms():
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((40, 32)).astype(np.float32)
+    b = (0.1 * rng.standard_normal(32)).astype(np.float32)
+    for got, want in ((O.route_scored(x, 4), O.route_topk(x, 4)),
+                      (O.route_scored(x, 4, "sigmoid", b, 8, 3, "top2", True, 2.5),
+                       O.route_topk_grouped(x, 4, 8, 3, b, 2.5))):
+        assert np.array_equal(got[0], want[0])
+        assert np.allclose(got[1], want[1], rtol=1e-12)
+
+
+def test_oracle_masks():
+    x = np.full((3, 6), -np.inf)
+    x[0, 4], x[1, 2], x[1, 5] = 1.0, np.nan, 3.0
+    ids, w = O.route_scored(x, 3, "softmax", np.array([0, 9.0, 0, 0, 0, 0]))
+    assert ids.tolist() == [[4, 0, 1], [5, 0, 1], [0, 1, 2]]
+    assert w.tolist() == [[1, 0, 0], [1, 0, 0], [0, 0, 0]]
+
+
+def _check(x, k, scoring, bias, ng, tg, gscore, renorm, scale, strided=0):
+    xd = x.cuda()
+    if strided:
+        wide = torch.full((x.shape[0], x.shape[1] + strided), 99.0, dtype=x.dtype, device="cuda")
+        wide[:, :x.shape[1]] = xd
+        xd = wide[:, :x.shape[1]]
+    ids, w = m.moe_route_scored(xd, k, scoring, None if bias is None else bias.cuda(), ng, tg, gscore, renorm, scale)
+    torch.cuda.synchronize()
+    xn = x.double().numpy()
+    rids, rw = O.route_scored(xn, k, scoring, None if bias is None else bias.numpy(), ng, tg, gscore, renorm, scale)
+    assert np.array_equal(ids.cpu().numpy(), rids)
+    live = np.where(np.isfinite(xn), xn, np.nan)
+    chosen = np.take_along_axis(live, rids.astype(np.int64), 1)
+    with np.errstate(all="ignore"):
+        ref = np.nanmax(np.where(np.isfinite(live), live, -1e30), axis=1, keepdims=True) if scoring == "softmax" else 0.0
+        D = np.nan_to_num(np.abs(chosen - ref), nan=0.0, posinf=0.0)
+    D = D.max(axis=1, keepdims=True) if x.shape[0] else D
+    tol = (2 if renorm else 1) * (D + 44) * 2.0 ** -24 * np.abs(rw)
+    assert np.all(np.abs(w.cpu().numpy().astype(np.float64) - rw) <= tol)
+
+
+CASES = [  # T, E, k, scoring, bias, groups, kept, group score, renorm
+    (1, 256, 8, "sigmoid", True, 8, 4, "top2", True),
+    (300, 256, 8, "sigmoid", True, 8, 4, "top2", True),
+    (129, 128, 4, "softmax", True, 1, 1, "max", False),
+    (64, 160, 6, "softmax", False, 8, 3, "max", False),
+    (65, 160, 6, "softmax", False, 8, 3, "top2", True),
+    (33, 1024, 32, "sigmoid", True, 32, 7, "max", True),
+    (31, 1024, 8, "softmax", True, 1, 1, "max", True),
+    (7, 1, 1, "softmax", False, 1, 1, "max", True),
+    (5, 33, 32, "sigmoid", False, 1, 1, "max", False),
+    (17, 12, 3, "sigmoid", True, 12, 3, "top2", True),
+    (40, 513, 5, "softmax", True, 27, 26, "top2", False),
+    (2000, 64, 6, "sigmoid", True, 4, 2, "max", True),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k,scoring,bias,ng,tg,gscore,renorm", CASES)
+@pytest.mark.parametrize("kind", ["normal", "ties", "bf16"])
+def test_matches_oracle(T, E, k, scoring, bias, ng, tg, gscore, renorm, kind):
+    g = torch.Generator().manual_seed(T * 31 + E)
+    x = torch.randn(T, E, generator=g) * 2
+    b = torch.randn(E, generator=g) * 0.05 if bias else None
+    if kind == "ties":                     # equal logits and equal biases: ties between experts and groups
+        x = torch.round(x)
+        b = torch.round(b * 10) / 8 if bias else None
+    if kind == "bf16":
+        x = x.bfloat16()
+    _check(x, k, scoring, b, ng, tg, gscore, renorm, 2.5, strided=3 if kind == "bf16" else 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("ng,tg,gscore", [(1, 1, "max"), (4, 2, "top2"), (4, 2, "max")])
+@pytest.mark.parametrize("bias", [False, True])
+def test_masked_experts(scoring, ng, tg, gscore, bias):
+    """-inf and NaN logits: some experts, all but one, a whole group, whole rows; +inf logits."""
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(64, 64, generator=g)
+    x[torch.rand(64, 64, generator=g) < 0.4] = float("-inf")
+    x[torch.rand(64, 64, generator=g) < 0.1] = float("nan")
+    x[3] = float("-inf")
+    x[4] = float("nan")
+    x[5] = float("-inf")
+    x[5, 37] = -2.0
+    x[6, 16:32] = float("-inf")
+    x[7, 9] = float("inf")
+    x[8, 2] = x[8, 50] = float("inf")
+    x[9] = float("inf")
+    b = torch.randn(64, generator=g) if bias else None
+    _check(x, 6, scoring, b, ng, tg, gscore, True, 1.0)
+    _check(x, 6, scoring, b, ng, tg, gscore, False, 1.5)
+
+
+@pytest.mark.gpu
+def test_large_and_close_scores():
+    """Saturated sigmoids, logits far apart, and sums s + b that differ by a few 2^-25."""
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(200, 96, generator=g) * 30
+    _check(x, 8, "softmax", None, 1, 1, "max", True, 1.0)
+    _check(x.clamp(-30, 30), 8, "sigmoid", torch.randn(96, generator=g) * 1e-3, 6, 3, "top2", True, 1.0)
+    # s + b = 1/2 + 1/8 for every expert up to the rounding of b to 32 bits
+    y = torch.randn(100, 64, generator=g)
+    s = torch.sigmoid(y[:1].double())
+    b = (0.625 - s[0]).float()
+    _check(y[:1].expand(100, 64).contiguous(), 8, "sigmoid", b, 1, 1, "max", True, 1.0)
+    _check(y[:1].expand(100, 64).contiguous(), 8, "sigmoid", b, 8, 4, "top2", True, 1.0)
+
+
+@pytest.mark.gpu
+def test_graph_and_streams():
+    """The call on a side stream, and captured and replayed on new logits."""
+    x = torch.randn(50, 64, device="cuda")
+    ids = torch.empty(50, 4, dtype=torch.int32, device="cuda")
+    w = torch.empty(50, 4, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    m.moe_route_scored(x, 4, ids=ids, w=w, stream=side)
+    torch.cuda.synchronize()
+    assert np.array_equal(ids.cpu().numpy(), O.route_scored(x.cpu().numpy(), 4)[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.moe_route_scored(x, 4, ids=ids, w=w)
+    x.copy_(torch.randn(50, 64))
+    g.replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(ids.cpu().numpy(), O.route_scored(x.cpu().numpy(), 4)[0])
