@@ -13,9 +13,9 @@
 // prepared so; the tokens' [rows, K/32] bytes may sit at any alignment, which no TMA copy takes, so
 // scale warps load them a stage of their own ahead, through registers.
 //
-// Warp roles: 0 producer, 1 MMA issuer (it also issues the scale copies into tensor memory, in
-// order with the MMAs that read them), 2..5 epilogue, then the scale warps. Waits are bounded as
-// in the other GEMMs.
+// Warp roles: 0 producer, 1 MMA issuer, 2..5 epilogue, then the scale warps, which also issue the
+// copies of both sides' scales into the stage's tensor-memory slot. Waits are bounded as in the
+// other GEMMs.
 #include <cmath>
 
 #include "gemm_common.cuh"
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT>::THREADS, 1)
     auto opB = [&](int s) { return smem + s * C::STAGE + C::B_OFF; };
     auto sfA = [&](int s) { return smem + s * C::STAGE + C::SFA_OFF; };
     auto sfB = [&](int s, int h, int rg) { return smem + s * C::STAGE + C::SFB_OFF + (h * C::RG + rg) * 512; };
-    uint64_t* sf_full = ctl->raw_full;  // the token scales of stage s are in shared memory
+    uint64_t* sf_full = ctl->raw_full;  // the scales of stage s are in tensor memory
     const int warp = warp_id(), lane = lane_id();
     const int G = a.G, NT = a.NT, KB = a.KB;
 
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT>::THREADS, 1)
             mbar_init(&ctl->tfull[b], 1);
             mbar_init(&ctl->tempty[b], 4);
         }
-        mbar_init(&ctl->drain[0], 1);
+        for (int i = 0; i <= kScaleWarps; ++i) mbar_init(&ctl->drain[i], 1);
         ctl->abort = 0;
         fence_barrier_init();
     }
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT>::THREADS, 1)
             ctl->abort = 1;
         }
     } else if (warp == 1) {
-        if (lane == 0) {  // ---------------- scale copies and MMAs
+        if (lane == 0) {  // ---------------- MMAs
             int s = 0, b = 0;
             uint32_t ph = 0, bph = 0;
             bool ok = true;
@@ -216,16 +216,6 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT>::THREADS, 1)
                     }
                     tc_fence_after();
                     const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + s * C::SF_SLOT), sfb = sfa + 8;
-                    const int halves = min(2, a.KS - 2 * kb);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (h < halves) {
-                            tmem_cp_32x128b_x4(sfa + 4 * h, sf_block_desc(smem_u32(sfA(s)) + 512 * h));
-#pragma unroll
-                            for (int rg = 0; rg < C::RG; ++rg)
-                                tmem_cp_32x128b_x4(sfb + 4 * (h * C::RG + rg), sf_block_desc(smem_u32(sfB(s, h, rg))));
-                        }
-                    }
                     const int steps = min(4, (a.K - kb * kStageK + 63) >> 6);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -293,9 +283,29 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT>::THREADS, 1)
                         reinterpret_cast<uint4*>(sfB(s, 1, rg))[lane] =
                             make_uint4(v[4 * rg].y, v[4 * rg + 1].y, v[4 * rg + 2].y, v[4 * rg + 3].y);
                     }
-                    fence_proxy_async_smem();
+                    fence_proxy_async_smem();  // the copies read these bytes through the async proxy
+                    if (!__all_sync(0xffffffffu, mbar_wait(&ctl->full[s], ph, abort_flag, a.wait_limit))) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        tc_fence_after();
+                        const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + s * C::SF_SLOT), sfb = sfa + 8;
+                        const int halves = min(2, a.KS - 2 * kb);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (h < halves) {
+                                tmem_cp_32x128b_x4(sfa + 4 * h, sf_block_desc(smem_u32(sfA(s)) + 512 * h));
+#pragma unroll
+                                for (int rg = 0; rg < C::RG; ++rg)
+                                    tmem_cp_32x128b_x4(sfb + 4 * (h * C::RG + rg),
+                                                       sf_block_desc(smem_u32(sfB(s, h, rg))));
+                            }
+                        }
+                        mma_commit(&sf_full[s]);
+                    }
+                    is.tc = true;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sf_full[s]);
                 }
                 if (++s == C::STAGES) {
                     s = 0;
@@ -350,7 +360,11 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT>::THREADS, 1)
     tc_fence_before();
     __syncthreads();
     if (*abort_flag) {
-        drain_in_flight(is, ctl->full, C::STAGES, warp == 1 && lane == 0 ? &ctl->drain[0] : nullptr);
+        drain_in_flight(is, ctl->full, C::STAGES,
+                        lane != 0                  ? nullptr
+                        : warp == 1                ? &ctl->drain[0]
+                        : warp >= C::SCALE_WARP0 ? &ctl->drain[1 + warp - C::SCALE_WARP0]
+                                                   : nullptr);
         tc_fence_before();
         __syncthreads();
     }
@@ -419,7 +433,11 @@ cudaError_t launch_gemm_mxf4(const Mxf4Problem& p, cudaStream_t st, bool pdl) {
     CUtensorMap tw;
     if (!make_map_codes(&tw, p.kdata, (uint64_t)Kp / 2, p.N, p.G)) return cudaErrorInvalidValue;
     const long long segs = std::max<long long>(1, std::min<long long>(p.G, p.M_alloc));
-    const double avg = (double)p.M_alloc / (double)segs, want = avg + 2.0 * std::sqrt(avg);
+    const double avg = (double)p.M_alloc / (double)segs;
+    // MOE_TOKEN_TILE=16|32|64|128|192 overrides the token-tile choice (tests, tuning)
+    const char* env = getenv("MOE_TOKEN_TILE");
+    const int v = env ? atoi(env) : 0;
+    const double want = v == 16 || v == 32 || v == 64 || v == 128 || v == 192 ? v : avg + 2.0 * std::sqrt(avg);
     if (want <= 16) return run_mxf4_bt<16>(p, tw, a, st, pdl);
     if (want <= 32) return run_mxf4_bt<32>(p, tw, a, st, pdl);
     if (want <= 64) return run_mxf4_bt<64>(p, tw, a, st, pdl);
