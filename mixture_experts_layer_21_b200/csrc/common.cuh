@@ -104,15 +104,6 @@ MOE_DEV void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, 
         "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
-// Four rows y0..y3 of a 2-D map whose box is one row high, one after the other in shared memory;
-// a row past the map's last reads as zero.
-MOE_DEV void tma_gather4(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y0, int y1, int y2, int y3) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(smem_u32(bar))
-        : "memory");
-}
 // The same two loads with an L2 cache policy (a createpolicy value; see l2_policy).
 MOE_DEV void tma_load_2d_hint(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, uint64_t pol) {
     asm volatile(
@@ -177,6 +168,8 @@ MOE_DEV void cp_async16_p(uint32_t dst_smem, const void* src, uint32_t src_bytes
     else
         cp_async16(dst_smem, src, src_bytes);
 }
+// Waits for all of this thread's cp.asyncs.
+MOE_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Arrive on an mbarrier (counted in its expected arrivals) once this thread's cp.asyncs land.
 MOE_DEV void cp_async_arrive_noinc(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -453,6 +446,23 @@ MOE_DEV void mma_commit_pair(uint64_t* bar, uint16_t mask) {
             smem_u32(bar)),
         "h"(mask)
         : "memory");
+}
+
+// kind::mxf4 over the pair (see mma_mxf4_ss): M = 256, B rows and the accumulator as above; each
+// CTA's tensor memory holds the scales of its own A rows and of all N rows of B.
+MOE_DEV void mma_mxf4_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                              uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+}
+// tmem_cp_32x128b_x4 in both CTAs of the pair, each from its own shared memory at this offset.
+MOE_DEV void tmem_cp_32x128b_x4_pair(uint32_t taddr, uint64_t src_desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(src_desc) : "memory");
 }
 
 // ---------------------------------------------------------------- e4m3 / MX staging

@@ -1861,30 +1861,6 @@ cudaError_t run_bf16(const GemmProblem& p, const GemmArgs& args, const CUtensorM
                     args);
 }
 
-// Pairs that can be resident at once (clusters of two CTAs, one CTA per SM), per device.
-template <typename Kern>
-int max_pairs_once(Kern kern, int smem, int threads, int (&cache)[64]) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (!cache[dev]) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * (num_sms() / 2));
-        cfg.blockDim = dim3(threads);
-        cfg.dynamicSmemBytes = smem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) return 0;
-        cache[dev] = n;
-    }
-    return cache[dev];
-}
-
 template <int BT, bool DUAL, int OUT, bool GATHER = false, bool FWD = true>
 cudaError_t run_pair(const GemmProblem& p, GemmArgs args, const CUtensorMap& tx, const CUtensorMap& t0,
                      const CUtensorMap& t1, cudaStream_t st, bool pdl) {

@@ -7,16 +7,30 @@
 // exact; the sum is fp32. Tiling as in the other grouped GEMMs ("swap AB"): a tile is 128 weight
 // rows (M) by up to BT token rows (N) of one segment, the MMA as wide as the tile's rows.
 //
-// A pipeline stage is 256 values of K: 128 bytes of packed codes per row on either side, loaded by
-// TMA with the 128-byte swizzle (the token rows by a gather of four rows per copy when row_idx is
-// given), and the stage's scales as 512-byte blocks in tensor-memory copy order. The weights' are
-// prepared so; the tokens' [rows, K/32] bytes may sit at any alignment, which no TMA copy takes, so
-// scale warps load them a stage of their own ahead, through registers.
+// A pipeline stage is 256 values of K: 128 bytes of packed codes per row on either side, in the
+// 128-byte swizzle, and the stage's scales as 512-byte blocks in tensor-memory copy order. The
+// weights come by TMA, and so do token rows in segment order. Token rows that row_idx gathers come
+// by cp.async from the token warps: the four-row TMA gather took about 80 cycles a copy, 1.15 ms
+// against 0.30 ms in segment order for 8192 rows x 4096 into 14336. The weights' scales are
+// prepared blocks; the tokens' [rows, K/32] bytes may sit at any alignment, which no TMA copy
+// takes, so the token warps load them through registers.
 //
-// Warp roles: 0 producer, 1 MMA issuer, 2..5 epilogue, then the scale warps, which also issue the
-// copies of both sides' scales into the stage's tensor-memory slot. Waits are bounded as in the
-// other GEMMs.
+// PAIR: two SMs per tile (a cluster of two CTAs, cta_group::2). A pair tile is 256 weight rows, 128
+// from each CTA's shared memory, by up to BT tokens, half of them from each, so an SM moves half the
+// token operand per product. The leader (rank 0) issues MMAs and scale copies for both.
+//
+// Warp roles: 0 producer, then one or two MMA issuers, four epilogue warps, four scale warps (they
+// take the stages in turn, bring the token scales into shared memory and issue the copies of both
+// sides' scales into the stage's tensor-memory slot; in the MMA thread those copies held up the
+// MMAs) and, with row_idx, four gather warps. Barriers, all with bounded waits as in the other GEMMs:
+//   full[s]    this CTA's copies of stage s landed
+//   pfull[s]   leader: the peer's copies and token scales of stage s are in place
+//   sf_full[s] leader: the scales of stage s are in tensor memory (of both CTAs)
+//   empty[s]   the MMAs that read stage s completed (both CTAs)
+//   tfull[b]   accumulator b holds a finished tile (both CTAs)
+//   tempty[b]  leader: the epilogues have drained accumulator b
 #include <cmath>
+#include <type_traits>
 
 #include "gemm_common.cuh"
 
@@ -26,14 +40,16 @@ namespace {
 
 constexpr int kStageK = 256;
 constexpr int kScaleWarps = 4;
+constexpr int kGatherWarps = 4;
 
 struct Mxf4Args {
     const int32_t* cu;
-    int G, N, K, KB, NT, M_alloc;
+    int G, N, K, KB, NT, NT1, M_alloc;  // NT1: 128-row weight blocks
     __nv_bfloat16* out;
     const float* alpha;
-    const uint8_t* w_sf;     // [G, NT, KS] blocks of 512 bytes, KS = blocks of 128 values
+    const uint8_t* w_sf;     // [G, NT1, KS] blocks of 512 bytes, KS = blocks of 128 values
     int KS;
+    const uint8_t* a_codes;  // [a_rows, K/2]
     const uint8_t* a_sf;     // [a_rows, K/32]
     int a_rows;
     const int32_t* row_idx;
@@ -42,25 +58,35 @@ struct Mxf4Args {
     int l2_w, l2_t;
 };
 
-template <int BT>
+template <int BT, bool GATHER, bool PAIR>
 struct Mxf4Cfg {
     static constexpr int A_BYTES = kTileN * kStageK / 2;
     static constexpr int B_OFF = A_BYTES;
-    static constexpr int B_BYTES = BT * kStageK / 2;
+    static constexpr int B_ROWS = PAIR ? BT / 2 : BT;           // this CTA's token rows
+    static constexpr int B_BYTES = B_ROWS * kStageK / 2;
     static constexpr int SFA_OFF = B_OFF + B_BYTES;             // two 512-byte blocks
     static constexpr int RG = (BT + 127) / 128;                 // 128-row groups of the token side
     static constexpr int SFB_OFF = SFA_OFF + 1024;              // [128-K half][row group] blocks
     static constexpr int STAGE = round1024(SFB_OFF + 2 * RG * 512);
+    // A thread issues a block-scaled MMA about every 145 cycles, so narrow tiles split each stage's
+    // four K steps between two issuers with partial sums of their own.
+    static constexpr int NI = BT <= 64 ? 2 : 1;
     static constexpr int SF_SLOT = 8 + 8 * RG;                  // TMEM columns of a stage's scales
-    static constexpr int SF_BASE = 2 * BT;                      // after two accumulators
+    static constexpr int SF_BASE = 2 * NI * BT;                 // after two accumulators
     static constexpr int STAGES = cmin(cmin(kMaxStages, kSmemBudget / STAGE), (512 - SF_BASE) / SF_SLOT);
     static constexpr int TMEM_COLS = tmem_cols_pow2(SF_BASE + STAGES * SF_SLOT);
-    static constexpr int SCALE_WARP0 = 6;
-    static constexpr int THREADS = (SCALE_WARP0 + kScaleWarps) * 32;
+    static constexpr int EPI_WARP0 = 1 + NI;
+    static constexpr int SCALE_WARP0 = EPI_WARP0 + 4;
+    static constexpr int GATHER_WARP0 = SCALE_WARP0 + kScaleWarps;
+    static constexpr int THREADS = (GATHER_WARP0 + (GATHER ? kGatherWarps : 0)) * 32;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE + kCtrlBytes;
+    static constexpr int TAB_OFF = (sizeof(CtrlBlock) + 15) / 16 * 16;  // gather warps' row tables
     static_assert(BT % 16 == 0 && BT >= 16 && BT <= 240, "token tile");
+    static_assert(!PAIR || (BT % 32 == 0 && NI == 1), "pair MMA N: a multiple of 32");
     static_assert(STAGES >= 3 && SMEM_BYTES <= kSmemLimit && SF_BASE + STAGES * SF_SLOT <= 512, "MXFP4 GEMM config");
-    static_assert(B_OFF % 1024 == 0 && SFA_OFF % 512 == 0, "operand alignment");
+    static_assert(B_OFF % 1024 == 0 && B_BYTES % 1024 == 0 && SFA_OFF % 512 == 0, "operand alignment");
+    static_assert(TAB_OFF + kGatherWarps * B_ROWS * 4 <= kCtrlBytes, "gather tables");
+    static_assert(NI + kScaleWarps <= 6, "drain barriers");
 };
 
 // The eight scale bytes of a row's stage, read at whatever alignment the row has; bytes past the
@@ -86,11 +112,11 @@ MOE_DEV uint2 load_scales8(const uint8_t* p, int n) {
     return make_uint2(w[0], w[1]);
 }
 
-template <int BT, bool GATHER>
-__global__ void __launch_bounds__(Mxf4Cfg<BT>::THREADS, 1)
+template <int BT, bool GATHER, bool PAIR>
+__global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
     grouped_gemm_mxf4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                              const Mxf4Args a) {
-    using C = Mxf4Cfg<BT>;
+    using C = Mxf4Cfg<BT, GATHER, PAIR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     CtrlBlock* ctl = reinterpret_cast<CtrlBlock*>(smem + C::STAGES * C::STAGE);
@@ -100,21 +126,34 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT>::THREADS, 1)
     auto opB = [&](int s) { return smem + s * C::STAGE + C::B_OFF; };
     auto sfA = [&](int s) { return smem + s * C::STAGE + C::SFA_OFF; };
     auto sfB = [&](int s, int h, int rg) { return smem + s * C::STAGE + C::SFB_OFF + (h * C::RG + rg) * 512; };
-    uint64_t* sf_full = ctl->raw_full;  // the scales of stage s are in tensor memory
+    uint64_t* sf_full = ctl->raw_full;
+    uint64_t* pfull = ctl->raw_empty;
     const int warp = warp_id(), lane = lane_id();
-    const int G = a.G, NT = a.NT, KB = a.KB;
+    const int G = a.G, NT = a.NT, KB = a.KB;  // NT: blocks of 128 weight rows, or of 256 (PAIR)
+    const int rank = PAIR ? (int)cluster_ctarank() : 0;
+    const bool leader = rank == 0;
+    const int first_tile = PAIR ? blockIdx.x >> 1 : blockIdx.x, tile_step = PAIR ? gridDim.x >> 1 : gridDim.x;
+    // the MMA's width for a tile's rows, and the first row of this CTA's part of the token operand
+    auto mma_n = [](int rows) { return PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; };
+    auto part0 = [&](int rows) { return rank * (mma_n(rows) / 2); };
+    // a barrier that the other CTA also arrives on is acquired at cluster scope
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return PAIR ? mbar_wait_cluster(bar, parity, abort_flag, a.wait_limit)
+                    : mbar_wait(bar, parity, abort_flag, a.wait_limit);
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&ctl->full[s], 1);
-            mbar_init(&ctl->empty[s], 1);
+            mbar_init(&ctl->full[s], GATHER ? 33 : 1);  // and the 32 lanes that copied the stage's token rows
+            mbar_init(&ctl->empty[s], C::NI);
             mbar_init(&sf_full[s], 1);
+            mbar_init(&pfull[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&ctl->tfull[b], 1);
-            mbar_init(&ctl->tempty[b], 4);
+            mbar_init(&ctl->tfull[b], C::NI);
+            mbar_init(&ctl->tempty[b], PAIR ? 8 : 4);
         }
-        for (int i = 0; i <= kScaleWarps; ++i) mbar_init(&ctl->drain[i], 1);
+        for (int i = 0; i < C::NI + kScaleWarps; ++i) mbar_init(&ctl->drain[i], 1);
         ctl->abort = 0;
         fence_barrier_init();
     }
@@ -123,118 +162,113 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT>::THREADS, 1)
         tma_prefetch_desc(&tm_w);
     }
     if (warp == 1) {
-        tmem_alloc(&ctl->tmem_slot, C::TMEM_COLS);
-        tmem_relinquish();
+        if (PAIR) {
+            tmem_alloc_pair(&ctl->tmem_slot, C::TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(&ctl->tmem_slot, C::TMEM_COLS);
+            tmem_relinquish();
+        }
     }
     pdl_wait();
     if (warp == 0) build_segment_table<BT>(a, ctl, lane);
     tc_fence_before();
-    __syncthreads();
+    if (PAIR) cluster_sync();  // both CTAs' barriers initialised and tensor memory allocated
+    else __syncthreads();
     tc_fence_after();
     pdl_launch();
     const uint32_t tmem_base = ctl->tmem_slot;
     const int total = ctl->tpre[G];
 
     if (warp == 0) {
-        // ---------------- producer: lane 0 the tiled copies, all lanes the gathered token rows
-        const uint64_t pol_w = l2_policy(a.l2_w), pol_t = l2_policy(a.l2_t);
-        int s = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
-            int g, nt, row0, rows;
-            decode_tile<BT>(L, ctl, G, NT, g, nt, row0, rows);
-            const uint8_t* wsf = a.w_sf + ((size_t)g * NT + nt) * a.KS * 512;
-            constexpr int Q = (BT / 4 + 31) / 32;  // gathers of four rows per lane
-            int idx[Q][4];
-            if (GATHER) {
-#pragma unroll
-                for (int q = 0; q < Q; ++q)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = (q * 32 + lane) * 4 + i;
-                        int v = r < rows ? a.row_idx[row0 + r] : a.a_rows;
-                        if (v < 0 || v > a.a_rows || (v == a.a_rows && r < rows)) {
-                            report_error(a.err, MOE_ERR_DEVICE, row0 + r);
-                            v = a.a_rows;  // past the last row: reads as zeros
-                        }
-                        idx[q][i] = v;
+        if (lane == 0) {  // ---------------- producer: weights and, in segment order, token rows
+            const uint64_t pol_w = l2_policy(a.l2_w), pol_t = l2_policy(a.l2_t);
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int L = first_tile; L < total && ok; L += tile_step) {
+                int g, nt, row0, rows;
+                decode_tile<BT>(L, ctl, G, NT, g, nt, row0, rows);
+                // A pair's second block past the last one reads as zeros by the tensor map; its
+                // scale copy repeats the last block's.
+                const int wb = PAIR ? 2 * nt + rank : nt;
+                const uint8_t* wsf = a.w_sf + ((size_t)g * a.NT1 + min(wb, a.NT1 - 1)) * a.KS * 512;
+                const int trow = row0 + part0(rows);
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!wait(&ctl->empty[s], ph ^ 1u)) {
+                        ok = false;
+                        break;
                     }
-            }
-            for (int kb = 0; kb < KB; ++kb) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&ctl->empty[s], ph ^ 1u, abort_flag, a.wait_limit))) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
                     const uint32_t sfn = min(1024, (a.KS - 2 * kb) * 512);
-                    mbar_arrive_expect_tx(&ctl->full[s], C::A_BYTES + C::B_BYTES + sfn);
-                    tma_load_3d_p(opA(s), &tm_w, &ctl->full[s], kb * (kStageK / 2), nt * kTileN, g, pol_w);
+                    mbar_arrive_expect_tx(&ctl->full[s], C::A_BYTES + (GATHER ? 0 : C::B_BYTES) + sfn);
+                    tma_load_3d_p(opA(s), &tm_w, &ctl->full[s], kb * (kStageK / 2), wb * kTileN, g, pol_w);
                     bulk_load_p(sfA(s), wsf + (size_t)kb * 1024, sfn, &ctl->full[s], pol_w);
-                    if (!GATHER) tma_load_2d_p(opB(s), &tm_a, &ctl->full[s], kb * (kStageK / 2), row0, pol_t);
+                    if (!GATHER) tma_load_2d_p(opB(s), &tm_a, &ctl->full[s], kb * (kStageK / 2), trow, pol_t);
                     is.mask |= 1u << s;
                     is.par = (is.par & ~(1u << s)) | (ph << s);
-                }
-                __syncwarp();
-                if (GATHER) {
-#pragma unroll
-                    for (int q = 0; q < Q; ++q)
-                        if ((q * 32 + lane) * 4 < BT)
-                            tma_gather4(opB(s) + (q * 32 + lane) * 512, &tm_a, &ctl->full[s], kb * (kStageK / 2),
-                                        idx[q][0], idx[q][1], idx[q][2], idx[q][3]);
-                }
-                if (++s == C::STAGES) {
-                    s = 0;
-                    ph ^= 1u;
+                    if (++s == C::STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
             }
+            if (!ok) {
+                report_error(a.err, MOE_ERR_TIMEOUT, 1);
+                ctl->abort = 1;
+            }
         }
-        if (!ok && lane == 0) {
-            report_error(a.err, MOE_ERR_TIMEOUT, 1);
-            ctl->abort = 1;
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {  // ---------------- MMAs
+    } else if (warp < C::EPI_WARP0) {
+        // ---------------- MMAs: issuer I takes its share of each stage's four K steps
+        auto issue = [&](auto first) {
+            constexpr int SHARE = 4 / C::NI, I = decltype(first)::value;
+            const uint64_t a0 = sw128_kmajor_desc(smem_u32(opA(0))), b0 = sw128_kmajor_desc(smem_u32(opB(0)));
             int s = 0, b = 0;
             uint32_t ph = 0, bph = 0;
             bool ok = true;
-            for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
+            for (int L = first_tile; L < total && ok; L += tile_step) {
                 int g, nt, row0, rows;
                 decode_tile<BT>(L, ctl, G, NT, g, nt, row0, rows);
-                const int n_mma = (rows + 15) & ~15;
-                if (!mbar_wait(&ctl->tempty[b], bph ^ 1u, abort_flag, a.wait_limit)) {
+                const uint32_t idesc = idesc_mxf4(PAIR ? 2 * kTileN : kTileN, mma_n(rows), 0);
+                constexpr uint32_t id2 = idesc_mxf4(0, 0, 2) ^ idesc_mxf4(0, 0, 0), at2 = 2u << 30;
+                if (!wait(&ctl->tempty[b], bph ^ 1u)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tmem_base + (uint32_t)(b * BT);
+                const uint32_t d = tmem_base + (uint32_t)((b * C::NI + I) * BT);
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!mbar_wait(&ctl->full[s], ph, abort_flag, a.wait_limit) ||
-                        !mbar_wait(&sf_full[s], ph, abort_flag, a.wait_limit)) {
+                    // operands landed in both CTAs and their scale factors are in tensor memory
+                    if (!wait(&ctl->full[s], ph) || (PAIR && !wait(&pfull[s], ph)) || !wait(&sf_full[s], ph)) {
                         ok = false;
                         break;
                     }
+                    if (GATHER) fence_proxy_async_smem();  // the gathered rows came by the generic proxy
                     tc_fence_after();
-                    const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + s * C::SF_SLOT), sfb = sfa + 8;
-                    const int steps = min(4, (a.K - kb * kStageK + 63) >> 6);
+                    const uint64_t as = a0 + (uint64_t)(s * (C::STAGE >> 4)), bs = b0 + (uint64_t)(s * (C::STAGE >> 4));
+                    const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + s * C::SF_SLOT);
+                    const int steps = (a.K - kb * kStageK + 63) >> 6;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int i = 0; i < SHARE; ++i) {
+                        const int j = I * SHARE + i;
                         if (j < steps) {
-                            const uint32_t id = (uint32_t)(j & 1) * 2, at = id << 30;
-                            mma_mxf4_ss(d, sw128_kmajor_desc(smem_u32(opA(s)) + 32 * j),
-                                        sw128_kmajor_desc(smem_u32(opB(s)) + 32 * j), idesc_mxf4(kTileN, n_mma, id),
-                                        (sfa + 4 * (j >> 1)) | at, (sfb + 4 * C::RG * (j >> 1)) | at, (kb | j) != 0);
+                            const uint32_t id = j & 1 ? idesc | id2 : idesc, at = j & 1 ? at2 : 0u;
+                            const uint32_t fa = (sfa + 4 * (j >> 1)) | at, fb = (sfa + 8 + 4 * C::RG * (j >> 1)) | at;
+                            const uint32_t acc = i ? 1u : (uint32_t)(kb != 0);
+                            if (PAIR) mma_mxf4_ss_pair(d, as + 2 * j, bs + 2 * j, id, fa, fb, acc);
+                            else mma_mxf4_ss(d, as + 2 * j, bs + 2 * j, id, fa, fb, acc);
                         }
                     }
                     is.tc = true;
-                    mma_commit(&ctl->empty[s]);
+                    if (PAIR) mma_commit_pair(&ctl->empty[s], 0x3);
+                    else mma_commit(&ctl->empty[s]);
                     if (++s == C::STAGES) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
                 if (!ok) break;
-                mma_commit(&ctl->tfull[b]);
+                if (PAIR) mma_commit_pair(&ctl->tfull[b], 0x3);
+                else mma_commit(&ctl->tfull[b]);
                 b ^= 1;
                 if (b == 0) bph ^= 1u;
             }
@@ -242,16 +276,68 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT>::THREADS, 1)
                 report_error(a.err, MOE_ERR_TIMEOUT, 2);
                 ctl->abort = 1;
             }
+        };
+        if (lane == 0 && leader) {
+            if (warp == 1) issue(std::integral_constant<int, 0>{});
+            else issue(std::integral_constant<int, C::NI - 1>{});
         }
-    } else if (warp >= C::SCALE_WARP0) {
-        // ---------------- scale warp i: the token scales of stages i, i + kScaleWarps, ...
+    } else if (warp < C::SCALE_WARP0) {
+        // ---------------- epilogue (four warps): lane = weight row, columns = tokens
+        const int q = warp & 3;
+        int b = 0;
+        uint32_t bph = 0;
+        for (int L = first_tile; L < total; L += tile_step) {
+            int g, nt, row0, rows;
+            decode_tile<BT>(L, ctl, G, NT, g, nt, row0, rows);
+            if (!wait(&ctl->tfull[b], bph)) {
+                if (lane == 0) report_error(a.err, MOE_ERR_TIMEOUT, 3);
+                ctl->abort = 1;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::NI * BT);
+            const int n = (PAIR ? 2 * nt + rank : nt) * kTileN + q * 32 + lane;
+            const float al = a.alpha ? a.alpha[g] : 1.0f;
+            for (int c0 = 0; c0 < rows; c0 += 16) {
+                uint32_t r[16];
+                tmem_ld16(tb + c0, r);
+                tmem_ld_wait();
+                if (C::NI == 2 && a.K > kStageK / 2) {  // the second issuer's partial sums (none for one half stage)
+                    uint32_t r1[16];
+                    tmem_ld16(tb + BT + c0, r1);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(r1[j]));
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (n < a.N && c0 + j < rows)
+                        a.out[(size_t)(row0 + c0 + j) * a.N + n] = __float2bfloat16_rn(__uint_as_float(r[j]) * al);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->tempty[b]), 0));
+                else mbar_arrive(&ctl->tempty[b]);
+            }
+            b ^= 1;
+            if (b == 0) bph ^= 1u;
+        }
+        // rows past the last segment are zero
+        const int start = ctl->cu[G - 1];
+        const long long n8 = (long long)(a.M_alloc - start) * (a.N / 8);
+        uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)start * a.N);
+        for (long long i = (long long)blockIdx.x * 128 + threadIdx.x - 32 * C::EPI_WARP0; i < n8; i += (long long)gridDim.x * 128)
+            o[i] = make_uint4(0u, 0u, 0u, 0u);
+    } else if (warp < C::GATHER_WARP0) {
+        // ---------------- scale warp: every kScaleWarps-th stage
         constexpr int NR = (BT + 31) / 32;  // rows per lane: lane, lane + 32, ...
         const int mine = warp - C::SCALE_WARP0;
         const int row_bytes = a.K / 32;
         int it = 0, s = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
+        for (int L = first_tile; L < total && ok; L += tile_step) {
             int g, nt, row0, rows;
             decode_tile<BT>(L, ctl, G, NT, g, nt, row0, rows);
             const uint8_t* src[NR];
@@ -261,7 +347,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT>::THREADS, 1)
                 src[i] = nullptr;
                 if (r < rows) {
                     const int v = GATHER ? a.row_idx[row0 + r] : row0 + r;
-                    if (v >= 0 && v < a.a_rows) src[i] = a.a_sf + (size_t)v * row_bytes;
+                    if (!GATHER || (v >= 0 && v < a.a_rows)) src[i] = a.a_sf + (size_t)v * row_bytes;
                 }
             }
             for (int kb = 0; kb < KB; ++kb, ++it) {
@@ -272,7 +358,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT>::THREADS, 1)
                         v[i] = make_uint2(0u, 0u);
                         if (i < NR && src[i < NR ? i : 0]) v[i] = load_scales8(src[i < NR ? i : 0] + kb * 8, row_bytes - kb * 8);
                     }
-                    if (!__all_sync(0xffffffffu, mbar_wait(&ctl->empty[s], ph ^ 1u, abort_flag, a.wait_limit))) {
+                    if (!__all_sync(0xffffffffu, wait(&ctl->empty[s], ph ^ 1u))) {
                         ok = false;
                         break;
                     }
@@ -284,27 +370,37 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT>::THREADS, 1)
                             make_uint4(v[4 * rg].y, v[4 * rg + 1].y, v[4 * rg + 2].y, v[4 * rg + 3].y);
                     }
                     fence_proxy_async_smem();  // the copies read these bytes through the async proxy
-                    if (!__all_sync(0xffffffffu, mbar_wait(&ctl->full[s], ph, abort_flag, a.wait_limit))) {
+                    __syncwarp();
+                    if (!__all_sync(0xffffffffu, wait(&ctl->full[s], ph) && (!PAIR || !leader || wait(&pfull[s], ph)))) {
                         ok = false;
                         break;
                     }
+                    if (GATHER && !leader) fence_proxy_async_smem();  // the peer's gathered rows, for the leader's MMAs
                     if (lane == 0) {
-                        tc_fence_after();
-                        const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + s * C::SF_SLOT), sfb = sfa + 8;
-                        const int halves = min(2, a.KS - 2 * kb);
+                        if (!leader) {
+                            mbar_arrive_cluster(mapa_shared(smem_u32(&pfull[s]), 0));
+                        } else {
+                            tc_fence_after();
+                            const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + s * C::SF_SLOT), sfb = sfa + 8;
+                            const int halves = min(2, a.KS - 2 * kb);
+                            auto copy = [](uint32_t t, uint64_t desc) {
+                                if (PAIR) tmem_cp_32x128b_x4_pair(t, desc);
+                                else tmem_cp_32x128b_x4(t, desc);
+                            };
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (h < halves) {
-                                tmem_cp_32x128b_x4(sfa + 4 * h, sf_block_desc(smem_u32(sfA(s)) + 512 * h));
+                            for (int h = 0; h < 2; ++h) {
+                                if (h < halves) {
+                                    copy(sfa + 4 * h, sf_block_desc(smem_u32(sfA(s)) + 512 * h));
 #pragma unroll
-                                for (int rg = 0; rg < C::RG; ++rg)
-                                    tmem_cp_32x128b_x4(sfb + 4 * (h * C::RG + rg),
-                                                       sf_block_desc(smem_u32(sfB(s, h, rg))));
+                                    for (int rg = 0; rg < C::RG; ++rg)
+                                        copy(sfb + 4 * (h * C::RG + rg), sf_block_desc(smem_u32(sfB(s, h, rg))));
+                                }
                             }
+                            if (PAIR) mma_commit_pair(&sf_full[s], 0x1);
+                            else mma_commit(&sf_full[s]);
+                            is.tc = true;
                         }
-                        mma_commit(&sf_full[s]);
                     }
-                    is.tc = true;
                     __syncwarp();
                 }
                 if (++s == C::STAGES) {
@@ -318,59 +414,94 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT>::THREADS, 1)
             ctl->abort = 1;
         }
     } else {
-        // ---------------- epilogue (warps 2..5): lane = weight row, columns = tokens
-        const int q = warp & 3;
-        int b = 0;
-        uint32_t bph = 0;
-        for (int L = blockIdx.x; L < total; L += gridDim.x) {
+        // ---------------- gather warp: the token rows of every kGatherWarps-th stage by cp.async. Lane
+        // 8 rr + c copies chunk c (16 bytes) of rows 4 i + rr, so that one instruction reads four whole
+        // 128-byte row pieces; chunk c of row r lands at c ^ (r % 8), the 128-byte swizzle. Rows past
+        // the tile's, without a source, and chunks past K are zeros.
+        const int mine = warp - C::GATHER_WARP0;
+        const int rr = lane >> 3, c = lane & 7;
+        int* tab = reinterpret_cast<int*>(reinterpret_cast<char*>(ctl) + C::TAB_OFF) + mine * C::B_ROWS;
+        const uint64_t pol_t = l2_policy(a.l2_t);
+        const int row_bytes = a.K / 2;
+        // rows 4 i + rr with even and odd i differ in bit 2 of the swizzle's row
+        const uint32_t sw0 = (uint32_t)(rr * 128 + ((c ^ rr) << 4)), sw1 = (uint32_t)(rr * 128 + ((c ^ (rr + 4)) << 4));
+        int it = 0, s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int L = first_tile; L < total && ok; L += tile_step) {
             int g, nt, row0, rows;
             decode_tile<BT>(L, ctl, G, NT, g, nt, row0, rows);
-            if (!mbar_wait(&ctl->tfull[b], bph, abort_flag, a.wait_limit)) {
-                if (lane == 0) report_error(a.err, MOE_ERR_TIMEOUT, 3);
-                ctl->abort = 1;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BT);
-            const int n = nt * kTileN + q * 32 + lane;
-            const float al = a.alpha ? a.alpha[g] : 1.0f;
-            for (int c0 = 0; c0 < rows; c0 += 16) {
-                uint32_t r[16];
-                tmem_ld16(tb + c0, r);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (n < a.N && c0 + j < rows)
-                        a.out[(size_t)(row0 + c0 + j) * a.N + n] = __float2bfloat16_rn(__uint_as_float(r[j]) * al);
-            }
-            tc_fence_before();
+            const int p0 = part0(rows), part = PAIR ? mma_n(rows) / 2 : mma_n(rows);  // 16 rows at least
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->tempty[b]);
-            b ^= 1;
-            if (b == 0) bph ^= 1u;
+            for (int i = lane; i < part; i += 32) {
+                int v = -1;
+                if (p0 + i < rows) {
+                    v = a.row_idx[row0 + p0 + i];
+                    if (v < 0 || v >= a.a_rows) {  // counts as a row of zeros
+                        report_error(a.err, MOE_ERR_DEVICE, row0 + p0 + i);
+                        v = -1;
+                    }
+                }
+                tab[i] = v;
+            }
+            __syncwarp();
+            for (int kb = 0; kb < KB; ++kb, ++it) {
+                if (it % kGatherWarps == mine) {
+                    if (!__all_sync(0xffffffffu, wait(&ctl->empty[s], ph ^ 1u))) {
+                        ok = false;
+                        break;
+                    }
+                    const int off = kb * (kStageK / 2) + c * 16;
+                    const bool in = off < row_bytes;
+                    const uint8_t* base = a.a_codes + (in ? off : 0);
+                    const uint32_t dst = smem_u32(opB(s));
+#pragma unroll 4
+                    for (int i = 0; i < part / 4; i += 2) {
+                        const int r0 = tab[4 * i + rr], r1 = tab[4 * i + 4 + rr];
+                        cp_async16_p(dst + i * 512 + sw0, base + (size_t)max(r0, 0) * row_bytes, in && r0 >= 0 ? 16u : 0u, pol_t);
+                        cp_async16_p(dst + i * 512 + 512 + sw1, base + (size_t)max(r1, 0) * row_bytes, in && r1 >= 0 ? 16u : 0u, pol_t);
+                    }
+                    cp_async_arrive_noinc(&ctl->full[s]);
+                }
+                if (++s == C::STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
         }
-        // rows past the last segment are zero
-        const int start = ctl->cu[G - 1];
-        const long long n8 = (long long)(a.M_alloc - start) * (a.N / 8);
-        uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)start * a.N);
-        for (long long i = (long long)blockIdx.x * 128 + threadIdx.x - 64; i < n8; i += (long long)gridDim.x * 128)
-            o[i] = make_uint4(0u, 0u, 0u, 0u);
+        cp_async_wait_all();
+        if (!ok && lane == 0) {
+            report_error(a.err, MOE_ERR_TIMEOUT, 7);
+            ctl->abort = 1;
+        }
     }
 
     tc_fence_before();
     __syncthreads();
-    if (*abort_flag) {
-        drain_in_flight(is, ctl->full, C::STAGES,
-                        lane != 0                  ? nullptr
-                        : warp == 1                ? &ctl->drain[0]
-                        : warp >= C::SCALE_WARP0 ? &ctl->drain[1 + warp - C::SCALE_WARP0]
-                                                   : nullptr);
+    uint64_t* drain = warp >= 1 && warp < C::EPI_WARP0                          ? &ctl->drain[warp - 1]
+                      : warp >= C::SCALE_WARP0 && warp < C::GATHER_WARP0 ? &ctl->drain[C::NI + warp - C::SCALE_WARP0]
+                                                                         : nullptr;
+    if (PAIR) {
+        // Whether or not anything aborted, every CTA lets what it has in flight finish (in a normal
+        // run these waits return at once), so that neither's memory is in use by the other.
+        int never = 0;
+        for (int q = 0; q < C::STAGES; ++q)
+            if (is.mask >> q & 1u) mbar_wait(&ctl->full[q], is.par >> q & 1u, &never);
+        if (is.tc) {
+            mma_commit_pair(drain, 0x1);
+            mbar_wait(drain, 0, &never);
+        }
+        tc_fence_before();
+        cluster_sync();
+    } else if (*abort_flag) {
+        drain_in_flight(is, ctl->full, C::STAGES, drain);
         tc_fence_before();
         __syncthreads();
     }
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, C::TMEM_COLS);
+        if (PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+        else tmem_dealloc(tmem_base, C::TMEM_COLS);
     }
 }
 
@@ -387,25 +518,35 @@ bool make_map_codes(CUtensorMap* m, const void* ptr, uint64_t bytes, uint64_t N,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BT, bool GATHER>
-cudaError_t run_mxf4(const CUtensorMap& ta, const CUtensorMap& tw, const Mxf4Args& a, cudaStream_t st, bool pdl) {
-    using C = Mxf4Cfg<BT>;
-    auto kern = grouped_gemm_mxf4_kernel<BT, GATHER>;
+template <int BT, bool GATHER, bool PAIR>
+cudaError_t run_mxf4(const CUtensorMap& ta, const CUtensorMap& tw, Mxf4Args a, cudaStream_t st, bool pdl) {
+    using C = Mxf4Cfg<BT, GATHER, PAIR>;
+    auto kern = grouped_gemm_mxf4_kernel<BT, GATHER, PAIR>;
     static int done[64] = {0};
     cudaError_t e = set_smem_once(kern, C::SMEM_BYTES, done);
     if (e != cudaSuccess) return e;
+    if (PAIR) {
+        static int pairs_cache[64] = {0};
+        const int maxp = max_pairs_once(kern, C::SMEM_BYTES, C::THREADS, pairs_cache);
+        if (maxp < 1) return cudaErrorInvalidConfiguration;
+        a.NT = (a.NT1 + 1) / 2;
+        const long long tiles = ((long long)(a.M_alloc + BT - 1) / BT + a.G) * a.NT;
+        const int pairs = (int)std::min<long long>(maxp, tiles);
+        return launch_k_pairs(kern, dim3(2 * pairs), dim3(C::THREADS), (size_t)C::SMEM_BYTES, st, pdl, ta, tw, a);
+    }
+    a.NT = a.NT1;
     const long long tiles = ((long long)(a.M_alloc + BT - 1) / BT + a.G) * a.NT;
     const int grid = (int)std::min<long long>(num_sms(), tiles);
     return launch_k(kern, dim3(grid), dim3(C::THREADS), (size_t)C::SMEM_BYTES, st, pdl, ta, tw, a);
 }
 
-template <int BT>
+template <int BT, bool PAIR = false>
 cudaError_t run_mxf4_bt(const Mxf4Problem& p, const CUtensorMap& tw, const Mxf4Args& a, cudaStream_t st, bool pdl) {
     CUtensorMap ta;
-    if (!make_map_u8(&ta, p.a_codes, (uint64_t)p.K / 2, p.a_rows, p.K / 2, kStageK / 2, p.row_idx ? 1 : BT,
+    if (!make_map_u8(&ta, p.a_codes, (uint64_t)p.K / 2, p.a_rows, p.K / 2, kStageK / 2, PAIR ? BT / 2 : BT,
                      CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    return p.row_idx ? run_mxf4<BT, true>(ta, tw, a, st, pdl) : run_mxf4<BT, false>(ta, tw, a, st, pdl);
+    return p.row_idx ? run_mxf4<BT, true, PAIR>(ta, tw, a, st, pdl) : run_mxf4<BT, false, PAIR>(ta, tw, a, st, pdl);
 }
 
 }  // namespace
@@ -418,12 +559,13 @@ cudaError_t launch_gemm_mxf4(const Mxf4Problem& p, cudaStream_t st, bool pdl) {
     a.N = p.N;
     a.K = p.K;
     a.KB = (p.K + kStageK - 1) / kStageK;
-    a.NT = (p.N + kTileN - 1) / kTileN;
+    a.NT1 = (p.N + kTileN - 1) / kTileN;
     a.M_alloc = p.M_alloc;
     a.out = static_cast<__nv_bfloat16*>(p.out);
     a.alpha = p.alpha;
     a.w_sf = static_cast<const uint8_t*>(p.kscale);
     a.KS = Kp / kMx8StageK;
+    a.a_codes = p.a_codes;
     a.a_sf = p.a_scales;
     a.a_rows = p.a_rows;
     a.row_idx = p.row_idx;
@@ -441,6 +583,8 @@ cudaError_t launch_gemm_mxf4(const Mxf4Problem& p, cudaStream_t st, bool pdl) {
     if (want <= 16) return run_mxf4_bt<16>(p, tw, a, st, pdl);
     if (want <= 32) return run_mxf4_bt<32>(p, tw, a, st, pdl);
     if (want <= 64) return run_mxf4_bt<64>(p, tw, a, st, pdl);
+    const char* pe = getenv("MOE_GEMM_PAIRS");
+    if (pe && pe[0] == '1') return run_mxf4_bt<192, true>(p, tw, a, st, pdl);
     if (want <= 128) return run_mxf4_bt<128>(p, tw, a, st, pdl);
     return run_mxf4_bt<192>(p, tw, a, st, pdl);
 }
