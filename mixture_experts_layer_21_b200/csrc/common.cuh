@@ -328,6 +328,21 @@ MOE_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
           "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
+// 16 lanes x 16 columns of 32 bits in the fragment layout of an 8-column matrix: thread t holds
+// rows t / 4 (r[0], r[1]) and t / 4 + 8 (r[2], r[3]) of columns 2 (t % 4) and + 1, then the same of
+// the next eight columns in r[4..7].
+MOE_DEV void tmem_ld_16x16(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+// Four 8 x 8 matrices of 16-bit values in that layout (two per register), each stored transposed:
+// lane 8 i + k gives the address of the 16 bytes that column k of matrix i goes to.
+MOE_DEV void stmatrix_x4_trans(uint32_t addr, uint32_t d0, uint32_t d1, uint32_t d2, uint32_t d3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(d0), "r"(d1),
+                 "r"(d2), "r"(d3)
+                 : "memory");
+}
 MOE_DEV void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // 32 lanes x 32-bit stores: 32 (x32) or 16 (x16) consecutive columns per thread.

@@ -73,21 +73,30 @@ struct Mxf4Cfg {
     static constexpr int NI = BT <= 64 ? 2 : 1;
     static constexpr int SF_SLOT = 8 + 8 * RG;                  // TMEM columns of a stage's scales
     static constexpr int SF_BASE = 2 * NI * BT;                 // after two accumulators
-    static constexpr int STAGES = cmin(cmin(kMaxStages, kSmemBudget / STAGE), (512 - SF_BASE) / SF_SLOT);
+    // after the stages: the control block, the gather warps' row tables, the epilogue's staging
+    static constexpr int TAB_OFF = (sizeof(CtrlBlock) + 15) / 16 * 16;
+    static constexpr int STAGING_OFF = (TAB_OFF + (GATHER ? kGatherWarps * B_ROWS * 4 : 0) + 127) / 128 * 128;
+    static constexpr int TAIL_BYTES = STAGING_OFF + 4 * 2048;
+    static constexpr int STAGES =
+        cmin(cmin(kMaxStages, (kSmemLimit - 1024 - TAIL_BYTES) / STAGE), (512 - SF_BASE) / SF_SLOT);
     static constexpr int TMEM_COLS = tmem_cols_pow2(SF_BASE + STAGES * SF_SLOT);
     static constexpr int EPI_WARP0 = 1 + NI;
     static constexpr int SCALE_WARP0 = EPI_WARP0 + 4;
     static constexpr int GATHER_WARP0 = SCALE_WARP0 + kScaleWarps;
     static constexpr int THREADS = (GATHER_WARP0 + (GATHER ? kGatherWarps : 0)) * 32;
-    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE + kCtrlBytes;
-    static constexpr int TAB_OFF = (sizeof(CtrlBlock) + 15) / 16 * 16;  // gather warps' row tables
+    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE + TAIL_BYTES;
     static_assert(BT % 16 == 0 && BT >= 16 && BT <= 240, "token tile");
     static_assert(!PAIR || (BT % 32 == 0 && NI == 1), "pair MMA N: a multiple of 32");
     static_assert(STAGES >= 3 && SMEM_BYTES <= kSmemLimit && SF_BASE + STAGES * SF_SLOT <= 512, "MXFP4 GEMM config");
     static_assert(B_OFF % 1024 == 0 && B_BYTES % 1024 == 0 && SFA_OFF % 512 == 0, "operand alignment");
-    static_assert(TAB_OFF + kGatherWarps * B_ROWS * 4 <= kCtrlBytes, "gather tables");
     static_assert(NI + kScaleWarps <= 6, "drain barriers");
 };
+
+MOE_DEV uint4 ld_shared16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 
 // The eight scale bytes of a row's stage, read at whatever alignment the row has; bytes past the
 // row's end are 0 (2^-127: their codes are zero).
@@ -283,7 +292,16 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
         }
     } else if (warp < C::SCALE_WARP0) {
         // ---------------- epilogue (four warps): lane = weight row, columns = tokens
+        // A warp's 32 weight rows of 32 tokens are transposed through its own 2 KB of shared memory (64
+        // bytes a token, the 16-byte pieces of token t at c ^ (t / 2 % 4) against bank conflicts), so that
+        // a store writes 64 contiguous bytes of eight tokens. Stores of two bytes a lane straight from
+        // the registers held the kernel at 228 us in the case above without any loads or MMAs.
         const int q = warp & 3;
+        const uint32_t stage = smem_u32(ctl) + C::STAGING_OFF + q * 2048;
+        // stmatrix: lane 8 i + k addresses token k + 8 (i / 2), 16-byte piece (i % 2) + 2 (row half)
+        const int st_t = (lane & 7) + 8 * (lane >> 4), st_c = (lane >> 3) & 1;
+        const uint32_t st0 = st_t * 64 + ((st_c ^ (st_t >> 1 & 3)) << 4), st1 = st_t * 64 + (((st_c + 2) ^ (st_t >> 1 & 3)) << 4);
+        const uint32_t ld0 = (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3 & 3)) << 4);  // token 8 i + lane / 4, piece lane % 4
         int b = 0;
         uint32_t bph = 0;
         for (int L = first_tile; L < total; L += tile_step) {
@@ -296,23 +314,50 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             }
             tc_fence_after();
             const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::NI * BT);
-            const int n = (PAIR ? 2 * nt + rank : nt) * kTileN + q * 32 + lane;
+            const int n0 = (PAIR ? 2 * nt + rank : nt) * kTileN + q * 32;
             const float al = a.alpha ? a.alpha[g] : 1.0f;
-            for (int c0 = 0; c0 < rows; c0 += 16) {
-                uint32_t r[16];
-                tmem_ld16(tb + c0, r);
+            const bool two = C::NI == 2 && a.K > kStageK / 2;  // the second issuer has sums (not for half a stage)
+#pragma unroll 1
+            for (int c0 = 0; c0 < rows; c0 += 32) {
+                const bool more = c0 + 16 < rows;  // the MMA wrote rows rounded up to 16
+                uint32_t r[4][8];                  // [16-token half][16-row half]
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < 2 || more) tmem_ld_16x16(tb + c0 + 16 * (i >> 1) + ((uint32_t)(16 * (i & 1)) << 16), r[i]);
                 tmem_ld_wait();
-                if (C::NI == 2 && a.K > kStageK / 2) {  // the second issuer's partial sums (none for one half stage)
-                    uint32_t r1[16];
-                    tmem_ld16(tb + BT + c0, r1);
+                if (two) {
+                    uint32_t r1[4][8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < 2 || more)
+                            tmem_ld_16x16(tb + BT + c0 + 16 * (i >> 1) + ((uint32_t)(16 * (i & 1)) << 16), r1[i]);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(r1[j]));
-                }
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (n < a.N && c0 + j < rows)
-                        a.out[(size_t)(row0 + c0 + j) * a.N + n] = __float2bfloat16_rn(__uint_as_float(r[j]) * al);
+                        for (int j = 0; j < 8; ++j)
+                            r[i][j] = __float_as_uint(__uint_as_float(r[i][j]) + __uint_as_float(r1[i][j]));
+                }
+                __syncwarp();  // the previous chunk has been read
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t d[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[i][2 * j]) * al,
+                                                                       __uint_as_float(r[i][2 * j + 1]) * al);
+                        d[j] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                    if (i < 2 || more) stmatrix_x4_trans(stage + 1024 * (i >> 1) + (i & 1 ? st1 : st0), d[0], d[1], d[2], d[3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = 8 * i + (lane >> 2), n = n0 + 8 * (lane & 3);
+                    const uint4 v = ld_shared16(stage + 512 * i + ld0);
+                    if (c0 + t < rows && n < a.N)
+                        *reinterpret_cast<uint4*>(a.out + (size_t)(row0 + c0 + t) * a.N + n) = v;
+                }
             }
             tc_fence_before();
             __syncwarp();
