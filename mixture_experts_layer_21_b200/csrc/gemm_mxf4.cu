@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
     auto sfB = [&](int s, int h, int rg) { return smem + s * C::STAGE + C::SFB_OFF + (h * C::RG + rg) * 512; };
     uint64_t* sf_full = ctl->raw_full;
     uint64_t* pfull = ctl->raw_empty;
-    const int warp = warp_id(), lane = lane_id();
+    const int warp = __shfl_sync(0xffffffffu, warp_id(), 0), lane = lane_id();
     const int G = a.G, NT = a.NT, KB = a.KB;  // NT: blocks of 128 weight rows, or of 256 (PAIR)
     const int rank = PAIR ? (int)cluster_ctarank() : 0;
     const bool leader = rank == 0;
@@ -145,10 +145,10 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
     // the MMA's width for a tile's rows, and the first row of this CTA's part of the token operand
     auto mma_n = [](int rows) { return PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; };
     auto part0 = [&](int rows) { return rank * (mma_n(rows) / 2); };
-    // a barrier that the other CTA also arrives on is acquired at cluster scope
+    // A whole warp's wait; a barrier that the other CTA also arrives on is acquired at cluster scope.
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return PAIR ? mbar_wait_cluster(bar, parity, abort_flag, a.wait_limit)
-                    : mbar_wait(bar, parity, abort_flag, a.wait_limit);
+        return __all_sync(0xffffffffu, PAIR ? mbar_wait_cluster(bar, parity, abort_flag, a.wait_limit)
+                                            : mbar_wait(bar, parity, abort_flag, a.wait_limit));
     };
 
     if (threadIdx.x == 0) {
@@ -186,45 +186,54 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
     else __syncthreads();
     tc_fence_after();
     pdl_launch();
-    const uint32_t tmem_base = ctl->tmem_slot;
-    const int total = ctl->tpre[G];
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, ctl->tmem_slot, 0);
+    const int total = __shfl_sync(0xffffffffu, ctl->tpre[G], 0);
+    // A tile's segment, weight block and rows, the same in every lane.
+    auto tile = [&](int L, int& g, int& nt, int& row0, int& rows) {
+        decode_tile<BT>(L, ctl, G, NT, g, nt, row0, rows);
+        g = __shfl_sync(0xffffffffu, g, 0);
+        nt = __shfl_sync(0xffffffffu, nt, 0);
+        row0 = __shfl_sync(0xffffffffu, row0, 0);
+        rows = __shfl_sync(0xffffffffu, rows, 0);
+    };
 
     if (warp == 0) {
-        if (lane == 0) {  // ---------------- producer: weights and, in segment order, token rows
-            const uint64_t pol_w = l2_policy(a.l2_w), pol_t = l2_policy(a.l2_t);
-            int s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int L = first_tile; L < total && ok; L += tile_step) {
-                int g, nt, row0, rows;
-                decode_tile<BT>(L, ctl, G, NT, g, nt, row0, rows);
-                // A pair's second block past the last one reads as zeros by the tensor map; its
-                // scale copy repeats the last block's.
-                const int wb = PAIR ? 2 * nt + rank : nt;
-                const uint8_t* wsf = a.w_sf + ((size_t)g * a.NT1 + min(wb, a.NT1 - 1)) * a.KS * 512;
-                const int trow = row0 + part0(rows);
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!wait(&ctl->empty[s], ph ^ 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sfn = min(1024, (a.KS - 2 * kb) * 512);
+        // ---------------- producer: weights and, in segment order, token rows
+        const uint64_t pol_w = l2_policy(a.l2_w), pol_t = l2_policy(a.l2_t);
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int L = first_tile; L < total && ok; L += tile_step) {
+            int g, nt, row0, rows;
+            tile(L, g, nt, row0, rows);
+            // A pair's second block past the last one reads as zeros by the tensor map; its
+            // scale copy repeats the last block's.
+            const int wb = PAIR ? 2 * nt + rank : nt;
+            const uint8_t* wsf = a.w_sf + ((size_t)g * a.NT1 + min(wb, a.NT1 - 1)) * a.KS * 512;
+            const int trow = row0 + part0(rows);
+            for (int kb = 0; kb < KB; ++kb) {
+                if (!wait(&ctl->empty[s], ph ^ 1u)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sfn = min(1024, (a.KS - 2 * kb) * 512);
+                if (elect_one()) {
                     mbar_arrive_expect_tx(&ctl->full[s], C::A_BYTES + (GATHER ? 0 : C::B_BYTES) + sfn);
                     tma_load_3d_p(opA(s), &tm_w, &ctl->full[s], kb * (kStageK / 2), wb * kTileN, g, pol_w);
                     bulk_load_p(sfA(s), wsf + (size_t)kb * 1024, sfn, &ctl->full[s], pol_w);
                     if (!GATHER) tma_load_2d_p(opB(s), &tm_a, &ctl->full[s], kb * (kStageK / 2), trow, pol_t);
-                    is.mask |= 1u << s;
-                    is.par = (is.par & ~(1u << s)) | (ph << s);
-                    if (++s == C::STAGES) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                }
+                is.mask |= 1u << s;
+                is.par = (is.par & ~(1u << s)) | (ph << s);
+                if (++s == C::STAGES) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
-            if (!ok) {
-                report_error(a.err, MOE_ERR_TIMEOUT, 1);
-                ctl->abort = 1;
-            }
+        }
+        if (!ok && lane == 0) {
+            report_error(a.err, MOE_ERR_TIMEOUT, 1);
+            ctl->abort = 1;
         }
     } else if (warp < C::EPI_WARP0) {
         // ---------------- MMAs: issuer I takes its share of each stage's four K steps
@@ -236,7 +245,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             bool ok = true;
             for (int L = first_tile; L < total && ok; L += tile_step) {
                 int g, nt, row0, rows;
-                decode_tile<BT>(L, ctl, G, NT, g, nt, row0, rows);
+                tile(L, g, nt, row0, rows);
                 const uint32_t idesc = idesc_mxf4(PAIR ? 2 * kTileN : kTileN, mma_n(rows), 0);
                 constexpr uint32_t id2 = idesc_mxf4(0, 0, 2) ^ idesc_mxf4(0, 0, 0), at2 = 2u << 30;
                 if (!wait(&ctl->tempty[b], bph ^ 1u)) {
@@ -256,37 +265,41 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                     const uint64_t as = a0 + (uint64_t)(s * (C::STAGE >> 4)), bs = b0 + (uint64_t)(s * (C::STAGE >> 4));
                     const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + s * C::SF_SLOT);
                     const int steps = (a.K - kb * kStageK + 63) >> 6;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < SHARE; ++i) {
-                        const int j = I * SHARE + i;
-                        if (j < steps) {
-                            const uint32_t id = j & 1 ? idesc | id2 : idesc, at = j & 1 ? at2 : 0u;
-                            const uint32_t fa = (sfa + 4 * (j >> 1)) | at, fb = (sfa + 8 + 4 * C::RG * (j >> 1)) | at;
-                            const uint32_t acc = i ? 1u : (uint32_t)(kb != 0);
-                            if (PAIR) mma_mxf4_ss_pair(d, as + 2 * j, bs + 2 * j, id, fa, fb, acc);
-                            else mma_mxf4_ss(d, as + 2 * j, bs + 2 * j, id, fa, fb, acc);
+                        for (int i = 0; i < SHARE; ++i) {
+                            const int j = I * SHARE + i;
+                            if (j < steps) {
+                                const uint32_t id = j & 1 ? idesc | id2 : idesc, at = j & 1 ? at2 : 0u;
+                                const uint32_t fa = (sfa + 4 * (j >> 1)) | at, fb = (sfa + 8 + 4 * C::RG * (j >> 1)) | at;
+                                const uint32_t acc = i ? 1u : (uint32_t)(kb != 0);
+                                if (PAIR) mma_mxf4_ss_pair(d, as + 2 * j, bs + 2 * j, id, fa, fb, acc);
+                                else mma_mxf4_ss(d, as + 2 * j, bs + 2 * j, id, fa, fb, acc);
+                            }
                         }
+                        is.tc = true;
+                        if (PAIR) mma_commit_pair(&ctl->empty[s], 0x3);
+                        else mma_commit(&ctl->empty[s]);
                     }
-                    is.tc = true;
-                    if (PAIR) mma_commit_pair(&ctl->empty[s], 0x3);
-                    else mma_commit(&ctl->empty[s]);
                     if (++s == C::STAGES) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
                 if (!ok) break;
-                if (PAIR) mma_commit_pair(&ctl->tfull[b], 0x3);
-                else mma_commit(&ctl->tfull[b]);
+                if (elect_one()) {
+                    if (PAIR) mma_commit_pair(&ctl->tfull[b], 0x3);
+                    else mma_commit(&ctl->tfull[b]);
+                }
                 b ^= 1;
                 if (b == 0) bph ^= 1u;
             }
-            if (!ok) {
+            if (!ok && lane == 0) {
                 report_error(a.err, MOE_ERR_TIMEOUT, 2);
                 ctl->abort = 1;
             }
         };
-        if (lane == 0 && leader) {
+        if (leader) {
             if (warp == 1) issue(std::integral_constant<int, 0>{});
             else issue(std::integral_constant<int, C::NI - 1>{});
         }
@@ -306,7 +319,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
         uint32_t bph = 0;
         for (int L = first_tile; L < total; L += tile_step) {
             int g, nt, row0, rows;
-            decode_tile<BT>(L, ctl, G, NT, g, nt, row0, rows);
+            tile(L, g, nt, row0, rows);
             if (!wait(&ctl->tfull[b], bph)) {
                 if (lane == 0) report_error(a.err, MOE_ERR_TIMEOUT, 3);
                 ctl->abort = 1;
@@ -384,7 +397,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
         bool ok = true;
         for (int L = first_tile; L < total && ok; L += tile_step) {
             int g, nt, row0, rows;
-            decode_tile<BT>(L, ctl, G, NT, g, nt, row0, rows);
+            tile(L, g, nt, row0, rows);
             const uint8_t* src[NR];
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
@@ -403,7 +416,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                         v[i] = make_uint2(0u, 0u);
                         if (i < NR && src[i < NR ? i : 0]) v[i] = load_scales8(src[i < NR ? i : 0] + kb * 8, row_bytes - kb * 8);
                     }
-                    if (!__all_sync(0xffffffffu, wait(&ctl->empty[s], ph ^ 1u))) {
+                    if (!wait(&ctl->empty[s], ph ^ 1u)) {
                         ok = false;
                         break;
                     }
@@ -416,12 +429,13 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                     }
                     fence_proxy_async_smem();  // the copies read these bytes through the async proxy
                     __syncwarp();
-                    if (!__all_sync(0xffffffffu, wait(&ctl->full[s], ph) && (!PAIR || !leader || wait(&pfull[s], ph)))) {
+                    if (!wait(&ctl->full[s], ph) || (PAIR && leader && !wait(&pfull[s], ph))) {
                         ok = false;
                         break;
                     }
                     if (GATHER && !leader) fence_proxy_async_smem();  // the peer's gathered rows, for the leader's MMAs
-                    if (lane == 0) {
+                    __syncwarp();
+                    if (elect_one()) {
                         if (!leader) {
                             mbar_arrive_cluster(mapa_shared(smem_u32(&pfull[s]), 0));
                         } else {
@@ -475,7 +489,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
         bool ok = true;
         for (int L = first_tile; L < total && ok; L += tile_step) {
             int g, nt, row0, rows;
-            decode_tile<BT>(L, ctl, G, NT, g, nt, row0, rows);
+            tile(L, g, nt, row0, rows);
             const int p0 = part0(rows), part = PAIR ? mma_n(rows) / 2 : mma_n(rows);  // 16 rows at least
             __syncwarp();
             for (int i = lane; i < part; i += 32) {
@@ -492,7 +506,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             __syncwarp();
             for (int kb = 0; kb < KB; ++kb, ++it) {
                 if (it % kGatherWarps == mine) {
-                    if (!__all_sync(0xffffffffu, wait(&ctl->empty[s], ph ^ 1u))) {
+                    if (!wait(&ctl->empty[s], ph ^ 1u)) {
                         ok = false;
                         break;
                     }
