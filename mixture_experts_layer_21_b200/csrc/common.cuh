@@ -405,6 +405,12 @@ MOE_DEV uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 MOE_DEV void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// The same without a release at cluster scope, which waits until every store of this thread, and it
+// seems of the SM, is visible to the cluster (about 1000 cycles under a storing epilogue): for
+// arrivals that announce what the tensor cores read or wrote, ordered by their own fences.
+MOE_DEV void mbar_arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 MOE_DEV bool mbar_try_wait_cluster(uint32_t bar_addr, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -491,6 +497,12 @@ MOE_DEV void mma_mxf4_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
 // tmem_cp_32x128b_x4 in both CTAs of the pair, each from its own shared memory at this offset.
 MOE_DEV void tmem_cp_32x128b_x4_pair(uint32_t taddr, uint64_t src_desc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(src_desc) : "memory");
+}
+
+// The same on this CTA's mbarrier alone.
+MOE_DEV void mma_commit_pair_here(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
 }
 
 // ---------------------------------------------------------------- e4m3 / MX staging

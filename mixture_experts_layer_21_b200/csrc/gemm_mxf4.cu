@@ -19,16 +19,23 @@
 // from each CTA's shared memory, by up to BT tokens, half of them from each, so an SM moves half the
 // token operand per product. The leader (rank 0) issues MMAs and scale copies for both.
 //
-// Warp roles: 0 producer, then one or two MMA issuers, four epilogue warps, four scale warps (they
-// take the stages in turn, bring the token scales into shared memory and issue the copies of both
-// sides' scales into the stage's tensor-memory slot; in the MMA thread those copies held up the
-// MMAs) and, with row_idx, four gather warps. Barriers, all with bounded waits as in the other GEMMs:
-//   full[s]    this CTA's copies of stage s landed
-//   pfull[s]   leader: the peer's copies and token scales of stage s are in place
-//   sf_full[s] leader: the scales of stage s are in tensor memory (of both CTAs)
-//   empty[s]   the MMAs that read stage s completed (both CTAs)
-//   tfull[b]   accumulator b holds a finished tile (both CTAs)
-//   tempty[b]  leader: the epilogues have drained accumulator b
+// The scales run ahead of the codes in a ring of their own, so that their way through registers,
+// shared and tensor memory is not in line with the codes' copies. Warp roles, each run by whole warps
+// with one lane elected to issue:
+//   producer   the codes of both sides into the stages (tokens only in segment order)
+//   MMA        one issuer, or two with partial sums of their own
+//   copier     scale blocks from the scale ring into tensor-memory slots
+//   epilogue   four warps: tensor memory -> alpha, bf16 -> out
+//   scales     four warps, taking the stages in turn: both sides' scale blocks into the scale ring
+//   gather     four warps, likewise (with row_idx): the token rows' codes by cp.async
+// Barriers, all with bounded waits as in the other GEMMs (s stage, d scale-ring entry, t slot, b buffer):
+//   full[s]      the TMA copies of stage s landed (PAIR: on the leader, both CTAs' copies)
+//   gfull[s]     this CTA's gathered rows of stage s landed; pfull[s], on the leader: the peer's
+//   empty[s]     the MMAs that read stage s completed (both CTAs)
+//   sf_ready[d]  this CTA's scale blocks are in the ring; psf[d], on the leader: the peer's
+//   sf_free[d]   they were copied (both CTAs)
+//   sf_full[t]   the scales are in tensor memory;  slot_free[t]  their MMAs completed
+//   tfull[b]     accumulator b holds a finished tile (both CTAs);  tempty[b]  it was read (leader)
 #include <cmath>
 #include <type_traits>
 
@@ -41,6 +48,25 @@ namespace {
 constexpr int kStageK = 256;
 constexpr int kScaleWarps = 4;
 constexpr int kGatherWarps = 4;
+constexpr int kSfRing = 8;
+
+// The control block with the barriers that only this kernel has.
+struct Mxf4Ctl {
+    CtrlBlock c;
+    uint64_t gfull[kMaxStages], sf_ready[kSfRing], psf[kSfRing], sf_free[kSfRing], sf_full[kSfRing], slot_free[kSfRing];
+};
+
+// A position in a ring of n entries and the parity of the current turn.
+struct Ring {
+    int i = 0;
+    uint32_t ph = 0;
+    MOE_DEV void next(int n) {
+        if (++i == n) {
+            i = 0;
+            ph ^= 1u;
+        }
+    }
+};
 
 struct Mxf4Args {
     const int32_t* cu;
@@ -61,35 +87,33 @@ struct Mxf4Args {
 template <int BT, bool GATHER, bool PAIR>
 struct Mxf4Cfg {
     static constexpr int A_BYTES = kTileN * kStageK / 2;
-    static constexpr int B_OFF = A_BYTES;
     static constexpr int B_ROWS = PAIR ? BT / 2 : BT;           // this CTA's token rows
     static constexpr int B_BYTES = B_ROWS * kStageK / 2;
-    static constexpr int SFA_OFF = B_OFF + B_BYTES;             // two 512-byte blocks
+    static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int RG = (BT + 127) / 128;                 // 128-row groups of the token side
-    static constexpr int SFB_OFF = SFA_OFF + 1024;              // [128-K half][row group] blocks
-    static constexpr int STAGE = round1024(SFB_OFF + 2 * RG * 512);
-    // A thread issues a block-scaled MMA about every 145 cycles, so narrow tiles split each stage's
-    // four K steps between two issuers with partial sums of their own.
+    static constexpr int SF_ENTRY = 1024 + 2 * RG * 512;        // weights' two blocks, tokens' [128-K half][row group]
+    // A thread issues block-scaled MMAs one after the other, each about 110 cycles however narrow, so
+    // narrow tiles split each stage's four K steps between two issuers with partial sums of their own.
     static constexpr int NI = BT <= 64 ? 2 : 1;
     static constexpr int SF_SLOT = 8 + 8 * RG;                  // TMEM columns of a stage's scales
     static constexpr int SF_BASE = 2 * NI * BT;                 // after two accumulators
-    // after the stages: the control block, the gather warps' row tables, the epilogue's staging
-    static constexpr int TAB_OFF = (sizeof(CtrlBlock) + 15) / 16 * 16;
+    static constexpr int SLOTS = cmin(kSfRing, (512 - SF_BASE) / SF_SLOT);
+    static constexpr int TMEM_COLS = tmem_cols_pow2(SF_BASE + SLOTS * SF_SLOT);
+    // behind the stages: the scale ring, the control block, the gather warps' row tables, the epilogue's staging
+    static constexpr int TAB_OFF = (sizeof(Mxf4Ctl) + 15) / 16 * 16;
     static constexpr int STAGING_OFF = (TAB_OFF + (GATHER ? kGatherWarps * B_ROWS * 4 : 0) + 127) / 128 * 128;
-    static constexpr int TAIL_BYTES = STAGING_OFF + 4 * 2048;
-    static constexpr int STAGES =
-        cmin(cmin(kMaxStages, (kSmemLimit - 1024 - TAIL_BYTES) / STAGE), (512 - SF_BASE) / SF_SLOT);
-    static constexpr int TMEM_COLS = tmem_cols_pow2(SF_BASE + STAGES * SF_SLOT);
-    static constexpr int EPI_WARP0 = 1 + NI;
+    static constexpr int TAIL_BYTES = kSfRing * SF_ENTRY + STAGING_OFF + 4 * 2048;
+    static constexpr int STAGES = cmin(kMaxStages, (kSmemLimit - 1024 - TAIL_BYTES) / STAGE);
+    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE + TAIL_BYTES;
+    static constexpr int COPIER_WARP = 1 + NI;
+    static constexpr int EPI_WARP0 = COPIER_WARP + 1;
     static constexpr int SCALE_WARP0 = EPI_WARP0 + 4;
     static constexpr int GATHER_WARP0 = SCALE_WARP0 + kScaleWarps;
     static constexpr int THREADS = (GATHER_WARP0 + (GATHER ? kGatherWarps : 0)) * 32;
-    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE + TAIL_BYTES;
     static_assert(BT % 16 == 0 && BT >= 16 && BT <= 240, "token tile");
     static_assert(!PAIR || (BT % 32 == 0 && NI == 1), "pair MMA N: a multiple of 32");
-    static_assert(STAGES >= 3 && SMEM_BYTES <= kSmemLimit && SF_BASE + STAGES * SF_SLOT <= 512, "MXFP4 GEMM config");
-    static_assert(B_OFF % 1024 == 0 && B_BYTES % 1024 == 0 && SFA_OFF % 512 == 0, "operand alignment");
-    static_assert(NI + kScaleWarps <= 6, "drain barriers");
+    static_assert(STAGES >= 3 && SLOTS >= 2 && SMEM_BYTES <= kSmemLimit && SF_BASE + SLOTS * SF_SLOT <= 512, "MXFP4 GEMM config");
+    static_assert(B_BYTES % 1024 == 0, "operand alignment");
 };
 
 MOE_DEV uint4 ld_shared16(uint32_t addr) {
@@ -128,15 +152,16 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
     using C = Mxf4Cfg<BT, GATHER, PAIR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    CtrlBlock* ctl = reinterpret_cast<CtrlBlock*>(smem + C::STAGES * C::STAGE);
+    uint8_t* sf_ring = smem + C::STAGES * C::STAGE;
+    Mxf4Ctl* mc = reinterpret_cast<Mxf4Ctl*>(sf_ring + kSfRing * C::SF_ENTRY);
+    CtrlBlock* ctl = &mc->c;
     volatile int* abort_flag = &ctl->abort;
     Issued is;
     auto opA = [&](int s) { return smem + s * C::STAGE; };
-    auto opB = [&](int s) { return smem + s * C::STAGE + C::B_OFF; };
-    auto sfA = [&](int s) { return smem + s * C::STAGE + C::SFA_OFF; };
-    auto sfB = [&](int s, int h, int rg) { return smem + s * C::STAGE + C::SFB_OFF + (h * C::RG + rg) * 512; };
-    uint64_t* sf_full = ctl->raw_full;
-    uint64_t* pfull = ctl->raw_empty;
+    auto opB = [&](int s) { return smem + s * C::STAGE + C::A_BYTES; };
+    auto sfA = [&](int d) { return sf_ring + d * C::SF_ENTRY; };
+    auto sfB = [&](int d, int h, int rg) { return sf_ring + d * C::SF_ENTRY + 1024 + (h * C::RG + rg) * 512; };
+    uint64_t* pfull = ctl->raw_full;
     const int warp = __shfl_sync(0xffffffffu, warp_id(), 0), lane = lane_id();
     const int G = a.G, NT = a.NT, KB = a.KB;  // NT: blocks of 128 weight rows, or of 256 (PAIR)
     const int rank = PAIR ? (int)cluster_ctarank() : 0;
@@ -145,24 +170,40 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
     // the MMA's width for a tile's rows, and the first row of this CTA's part of the token operand
     auto mma_n = [](int rows) { return PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; };
     auto part0 = [&](int rows) { return rank * (mma_n(rows) / 2); };
-    // A whole warp's wait; a barrier that the other CTA also arrives on is acquired at cluster scope.
+    // A whole warp's wait, with acquire at this CTA's scope also where the other CTA of a pair arrives:
+    // what such an arrival announces is read by the tensor cores alone, and acquires at cluster scope
+    // made the pair's barriers alone take 396 us of the 14336 x 4096 case (8192 rows), against 93.
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, PAIR ? mbar_wait_cluster(bar, parity, abort_flag, a.wait_limit)
-                                            : mbar_wait(bar, parity, abort_flag, a.wait_limit));
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_limit));
+    };
+    auto commit = [](uint64_t* bar) {  // in both CTAs of a pair
+        if (PAIR) mma_commit_pair(bar, 0x3);
+        else mma_commit(bar);
+    };
+    auto commit_here = [](uint64_t* bar) {
+        if (PAIR) mma_commit_pair_here(bar);
+        else mma_commit(bar);
     };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&ctl->full[s], GATHER ? 33 : 1);  // and the 32 lanes that copied the stage's token rows
+            mbar_init(&ctl->full[s], 1);
             mbar_init(&ctl->empty[s], C::NI);
-            mbar_init(&sf_full[s], 1);
+            mbar_init(&mc->gfull[s], 32);  // the lanes of the gather warp that copied the stage's rows
             mbar_init(&pfull[s], 1);
+        }
+        for (int d = 0; d < kSfRing; ++d) {
+            mbar_init(&mc->sf_ready[d], 2);  // the weights' copy and the tokens' scale warp
+            mbar_init(&mc->psf[d], 1);
+            mbar_init(&mc->sf_free[d], 1);
+            mbar_init(&mc->sf_full[d], 1);
+            mbar_init(&mc->slot_free[d], C::NI);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl->tfull[b], C::NI);
             mbar_init(&ctl->tempty[b], PAIR ? 8 : 4);
         }
-        for (int i = 0; i < C::NI + kScaleWarps; ++i) mbar_init(&ctl->drain[i], 1);
+        for (int i = 0; i <= C::NI; ++i) mbar_init(&ctl->drain[i], 1);
         ctl->abort = 0;
         fence_barrier_init();
     }
@@ -196,52 +237,56 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
         row0 = __shfl_sync(0xffffffffu, row0, 0);
         rows = __shfl_sync(0xffffffffu, rows, 0);
     };
+    auto give_up = [&](int site) {  // this warp's wait ran out, or another's did
+        if (lane == 0) {
+            report_error(a.err, MOE_ERR_TIMEOUT, site);
+            ctl->abort = 1;
+        }
+    };
 
     if (warp == 0) {
-        // ---------------- producer: weights and, in segment order, token rows
+        // ---------------- producer
         const uint64_t pol_w = l2_policy(a.l2_w), pol_t = l2_policy(a.l2_t);
-        int s = 0;
-        uint32_t ph = 0;
+        constexpr uint32_t BYTES = C::A_BYTES + (GATHER ? 0 : C::B_BYTES);
+        Ring st;
         bool ok = true;
         for (int L = first_tile; L < total && ok; L += tile_step) {
             int g, nt, row0, rows;
             tile(L, g, nt, row0, rows);
-            // A pair's second block past the last one reads as zeros by the tensor map; its
-            // scale copy repeats the last block's.
-            const int wb = PAIR ? 2 * nt + rank : nt;
-            const uint8_t* wsf = a.w_sf + ((size_t)g * a.NT1 + min(wb, a.NT1 - 1)) * a.KS * 512;
+            const int wrow = (PAIR ? 2 * nt + rank : nt) * kTileN;  // a block past the last reads as zeros
             const int trow = row0 + part0(rows);
             for (int kb = 0; kb < KB; ++kb) {
-                if (!wait(&ctl->empty[s], ph ^ 1u)) {
+                if (!wait(&ctl->empty[st.i], st.ph ^ 1u)) {
                     ok = false;
                     break;
                 }
-                const uint32_t sfn = min(1024, (a.KS - 2 * kb) * 512);
+                const int s = st.i, x = kb * (kStageK / 2);
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&ctl->full[s], C::A_BYTES + (GATHER ? 0 : C::B_BYTES) + sfn);
-                    tma_load_3d_p(opA(s), &tm_w, &ctl->full[s], kb * (kStageK / 2), wb * kTileN, g, pol_w);
-                    bulk_load_p(sfA(s), wsf + (size_t)kb * 1024, sfn, &ctl->full[s], pol_w);
-                    if (!GATHER) tma_load_2d_p(opB(s), &tm_a, &ctl->full[s], kb * (kStageK / 2), trow, pol_t);
+                    if (PAIR) {
+                        const uint32_t bar = mapa_shared(smem_u32(&ctl->full[s]), 0);  // the leader's
+                        if (leader) mbar_arrive_expect_tx(&ctl->full[s], 2 * BYTES);
+                        tma_load_3d_pair(opA(s), &tm_w, bar, x, wrow, g);
+                        if (!GATHER) tma_load_2d_pair(opB(s), &tm_a, bar, x, trow);
+                    } else {
+                        mbar_arrive_expect_tx(&ctl->full[s], BYTES);
+                        tma_load_3d_p(opA(s), &tm_w, &ctl->full[s], x, wrow, g, pol_w);
+                        if (!GATHER) tma_load_2d_p(opB(s), &tm_a, &ctl->full[s], x, trow, pol_t);
+                    }
                 }
                 is.mask |= 1u << s;
-                is.par = (is.par & ~(1u << s)) | (ph << s);
-                if (++s == C::STAGES) {
-                    s = 0;
-                    ph ^= 1u;
-                }
+                is.par = (is.par & ~(1u << s)) | (st.ph << s);
+                st.next(C::STAGES);
             }
         }
-        if (!ok && lane == 0) {
-            report_error(a.err, MOE_ERR_TIMEOUT, 1);
-            ctl->abort = 1;
-        }
-    } else if (warp < C::EPI_WARP0) {
+        if (!ok) give_up(1);
+    } else if (warp < C::COPIER_WARP) {
         // ---------------- MMAs: issuer I takes its share of each stage's four K steps
         auto issue = [&](auto first) {
             constexpr int SHARE = 4 / C::NI, I = decltype(first)::value;
             const uint64_t a0 = sw128_kmajor_desc(smem_u32(opA(0))), b0 = sw128_kmajor_desc(smem_u32(opB(0)));
-            int s = 0, b = 0;
-            uint32_t ph = 0, bph = 0;
+            Ring st, sl;
+            int b = 0;
+            uint32_t bph = 0;
             bool ok = true;
             for (int L = first_tile; L < total && ok; L += tile_step) {
                 int g, nt, row0, rows;
@@ -255,15 +300,15 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)((b * C::NI + I) * BT);
                 for (int kb = 0; kb < KB; ++kb) {
-                    // operands landed in both CTAs and their scale factors are in tensor memory
-                    if (!wait(&ctl->full[s], ph) || (PAIR && !wait(&pfull[s], ph)) || !wait(&sf_full[s], ph)) {
+                    if (!wait(&mc->sf_full[sl.i], sl.ph) || !wait(&ctl->full[st.i], st.ph) ||
+                        (GATHER && !wait(&mc->gfull[st.i], st.ph)) || (GATHER && PAIR && !wait(&pfull[st.i], st.ph))) {
                         ok = false;
                         break;
                     }
                     if (GATHER) fence_proxy_async_smem();  // the gathered rows came by the generic proxy
                     tc_fence_after();
-                    const uint64_t as = a0 + (uint64_t)(s * (C::STAGE >> 4)), bs = b0 + (uint64_t)(s * (C::STAGE >> 4));
-                    const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + s * C::SF_SLOT);
+                    const uint64_t as = a0 + (uint64_t)(st.i * (C::STAGE >> 4)), bs = b0 + (uint64_t)(st.i * (C::STAGE >> 4));
+                    const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + sl.i * C::SF_SLOT);
                     const int steps = (a.K - kb * kStageK + 63) >> 6;
                     if (elect_one()) {
 #pragma unroll
@@ -278,31 +323,81 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                             }
                         }
                         is.tc = true;
-                        if (PAIR) mma_commit_pair(&ctl->empty[s], 0x3);
-                        else mma_commit(&ctl->empty[s]);
+                        commit(&ctl->empty[st.i]);
+                        commit_here(&mc->slot_free[sl.i]);
                     }
-                    if (++s == C::STAGES) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                    st.next(C::STAGES);
+                    sl.next(C::SLOTS);
                 }
                 if (!ok) break;
-                if (elect_one()) {
-                    if (PAIR) mma_commit_pair(&ctl->tfull[b], 0x3);
-                    else mma_commit(&ctl->tfull[b]);
-                }
+                if (elect_one()) commit(&ctl->tfull[b]);
                 b ^= 1;
                 if (b == 0) bph ^= 1u;
             }
-            if (!ok && lane == 0) {
-                report_error(a.err, MOE_ERR_TIMEOUT, 2);
-                ctl->abort = 1;
-            }
+            if (!ok) give_up(2);
         };
         if (leader) {
             if (warp == 1) issue(std::integral_constant<int, 0>{});
             else issue(std::integral_constant<int, C::NI - 1>{});
+        } else if (GATHER && warp == 1) {
+            // peer: tells the leader that its gathered rows of each stage landed
+            Ring st;
+            bool ok = true;
+            for (int L = first_tile; L < total && ok; L += tile_step) {
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!wait(&mc->gfull[st.i], st.ph)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (elect_one()) mbar_arrive_remote(mapa_shared(smem_u32(&pfull[st.i]), 0));
+                    st.next(C::STAGES);
+                }
+            }
+            if (!ok) give_up(6);
         }
+    } else if (warp == C::COPIER_WARP) {
+        // ---------------- scale blocks: ring -> tensor memory (peer: tells the leader they are in its ring)
+        Ring rg, sl;
+        bool ok = true;
+        for (int L = first_tile; L < total && ok; L += tile_step) {
+            for (int kb = 0; kb < KB; ++kb) {
+                if (!wait(&mc->sf_ready[rg.i], rg.ph) ||
+                    (leader && ((PAIR && !wait(&mc->psf[rg.i], rg.ph)) || !wait(&mc->slot_free[sl.i], sl.ph ^ 1u)))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (elect_one()) {
+                    if (!leader) {
+                        mbar_arrive_remote(mapa_shared(smem_u32(&mc->psf[rg.i]), 0));
+                    } else {
+                        const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + sl.i * C::SF_SLOT), sfb = sfa + 8;
+                        const int halves = min(2, a.KS - 2 * kb);
+                        auto copy = [](uint32_t t, uint64_t desc) {
+                            if (PAIR) tmem_cp_32x128b_x4_pair(t, desc);
+                            else tmem_cp_32x128b_x4(t, desc);
+                        };
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (h < halves) {
+                                copy(sfa + 4 * h, sf_block_desc(smem_u32(sfA(rg.i)) + 512 * h));
+#pragma unroll
+                                for (int r = 0; r < C::RG; ++r)
+                                    copy(sfb + 4 * (h * C::RG + r), sf_block_desc(smem_u32(sfB(rg.i, h, r))));
+                            }
+                        }
+                        is.tc = true;
+                        commit_here(&mc->sf_full[sl.i]);
+                        commit(&mc->sf_free[rg.i]);
+                    }
+                }
+                rg.next(kSfRing);
+                sl.next(C::SLOTS);
+            }
+        }
+        if (!ok) give_up(4);
     } else if (warp < C::SCALE_WARP0) {
         // ---------------- epilogue (four warps): lane = weight row, columns = tokens
         // A warp's 32 weight rows of 32 tokens are transposed through its own 2 KB of shared memory (64
@@ -310,7 +405,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
         // a store writes 64 contiguous bytes of eight tokens. Stores of two bytes a lane straight from
         // the registers held the kernel at 228 us in the case above without any loads or MMAs.
         const int q = warp & 3;
-        const uint32_t stage = smem_u32(ctl) + C::STAGING_OFF + q * 2048;
+        const uint32_t stage = smem_u32(mc) + C::STAGING_OFF + q * 2048;
         // stmatrix: lane 8 i + k addresses token k + 8 (i / 2), 16-byte piece (i % 2) + 2 (row half)
         const int st_t = (lane & 7) + 8 * (lane >> 4), st_c = (lane >> 3) & 1;
         const uint32_t st0 = st_t * 64 + ((st_c ^ (st_t >> 1 & 3)) << 4), st1 = st_t * 64 + (((st_c + 2) ^ (st_t >> 1 & 3)) << 4);
@@ -321,8 +416,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             int g, nt, row0, rows;
             tile(L, g, nt, row0, rows);
             if (!wait(&ctl->tfull[b], bph)) {
-                if (lane == 0) report_error(a.err, MOE_ERR_TIMEOUT, 3);
-                ctl->abort = 1;
+                give_up(3);
                 break;
             }
             tc_fence_after();
@@ -375,7 +469,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->tempty[b]), 0));
+                if (PAIR) mbar_arrive_remote(mapa_shared(smem_u32(&ctl->tempty[b]), 0));
                 else mbar_arrive(&ctl->tempty[b]);
             }
             b ^= 1;
@@ -392,12 +486,16 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
         constexpr int NR = (BT + 31) / 32;  // rows per lane: lane, lane + 32, ...
         const int mine = warp - C::SCALE_WARP0;
         const int row_bytes = a.K / 32;
-        int it = 0, s = 0;
-        uint32_t ph = 0;
+        const uint64_t pol_w = l2_policy(a.l2_w);
+        int it = 0;
+        Ring rg;
         bool ok = true;
         for (int L = first_tile; L < total && ok; L += tile_step) {
             int g, nt, row0, rows;
             tile(L, g, nt, row0, rows);
+            // a pair's second block past the last one repeats the last block's scales (its codes are zeros)
+            const int wb = min(PAIR ? 2 * nt + rank : nt, a.NT1 - 1);
+            const uint8_t* wsf = a.w_sf + ((size_t)g * a.NT1 + wb) * a.KS * 512;
             const uint8_t* src[NR];
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
@@ -410,68 +508,39 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             }
             for (int kb = 0; kb < KB; ++kb, ++it) {
                 if (it % kScaleWarps == mine) {
+                    const int d = rg.i;
                     uint2 v[4 * C::RG];
 #pragma unroll
                     for (int i = 0; i < 4 * C::RG; ++i) {
                         v[i] = make_uint2(0u, 0u);
                         if (i < NR && src[i < NR ? i : 0]) v[i] = load_scales8(src[i < NR ? i : 0] + kb * 8, row_bytes - kb * 8);
                     }
-                    if (!wait(&ctl->empty[s], ph ^ 1u)) {
+                    if (!wait(&mc->sf_free[d], rg.ph ^ 1u)) {
                         ok = false;
                         break;
                     }
+                    if (elect_one()) {
+                        const uint32_t bytes = min(1024, (a.KS - 2 * kb) * 512);
+                        mbar_arrive_expect_tx(&mc->sf_ready[d], bytes);
+                        bulk_load_p(sfA(d), wsf + (size_t)kb * 1024, bytes, &mc->sf_ready[d], pol_w);
+                    }
+                    is.mask |= 1u << d;
+                    is.par = (is.par & ~(1u << d)) | (rg.ph << d);
 #pragma unroll
-                    for (int rg = 0; rg < C::RG; ++rg) {
-                        reinterpret_cast<uint4*>(sfB(s, 0, rg))[lane] =
-                            make_uint4(v[4 * rg].x, v[4 * rg + 1].x, v[4 * rg + 2].x, v[4 * rg + 3].x);
-                        reinterpret_cast<uint4*>(sfB(s, 1, rg))[lane] =
-                            make_uint4(v[4 * rg].y, v[4 * rg + 1].y, v[4 * rg + 2].y, v[4 * rg + 3].y);
+                    for (int r = 0; r < C::RG; ++r) {
+                        reinterpret_cast<uint4*>(sfB(d, 0, r))[lane] =
+                            make_uint4(v[4 * r].x, v[4 * r + 1].x, v[4 * r + 2].x, v[4 * r + 3].x);
+                        reinterpret_cast<uint4*>(sfB(d, 1, r))[lane] =
+                            make_uint4(v[4 * r].y, v[4 * r + 1].y, v[4 * r + 2].y, v[4 * r + 3].y);
                     }
                     fence_proxy_async_smem();  // the copies read these bytes through the async proxy
                     __syncwarp();
-                    if (!wait(&ctl->full[s], ph) || (PAIR && leader && !wait(&pfull[s], ph))) {
-                        ok = false;
-                        break;
-                    }
-                    if (GATHER && !leader) fence_proxy_async_smem();  // the peer's gathered rows, for the leader's MMAs
-                    __syncwarp();
-                    if (elect_one()) {
-                        if (!leader) {
-                            mbar_arrive_cluster(mapa_shared(smem_u32(&pfull[s]), 0));
-                        } else {
-                            tc_fence_after();
-                            const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + s * C::SF_SLOT), sfb = sfa + 8;
-                            const int halves = min(2, a.KS - 2 * kb);
-                            auto copy = [](uint32_t t, uint64_t desc) {
-                                if (PAIR) tmem_cp_32x128b_x4_pair(t, desc);
-                                else tmem_cp_32x128b_x4(t, desc);
-                            };
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                if (h < halves) {
-                                    copy(sfa + 4 * h, sf_block_desc(smem_u32(sfA(s)) + 512 * h));
-#pragma unroll
-                                    for (int rg = 0; rg < C::RG; ++rg)
-                                        copy(sfb + 4 * (h * C::RG + rg), sf_block_desc(smem_u32(sfB(s, h, rg))));
-                                }
-                            }
-                            if (PAIR) mma_commit_pair(&sf_full[s], 0x1);
-                            else mma_commit(&sf_full[s]);
-                            is.tc = true;
-                        }
-                    }
-                    __syncwarp();
+                    if (elect_one()) mbar_arrive(&mc->sf_ready[d]);
                 }
-                if (++s == C::STAGES) {
-                    s = 0;
-                    ph ^= 1u;
-                }
+                rg.next(kSfRing);
             }
         }
-        if (!ok && lane == 0) {
-            report_error(a.err, MOE_ERR_TIMEOUT, 5);
-            ctl->abort = 1;
-        }
+        if (!ok) give_up(5);
     } else {
         // ---------------- gather warp: the token rows of every kGatherWarps-th stage by cp.async. Lane
         // 8 rr + c copies chunk c (16 bytes) of rows 4 i + rr, so that one instruction reads four whole
@@ -479,13 +548,13 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
         // the tile's, without a source, and chunks past K are zeros.
         const int mine = warp - C::GATHER_WARP0;
         const int rr = lane >> 3, c = lane & 7;
-        int* tab = reinterpret_cast<int*>(reinterpret_cast<char*>(ctl) + C::TAB_OFF) + mine * C::B_ROWS;
+        int* tab = reinterpret_cast<int*>(reinterpret_cast<char*>(mc) + C::TAB_OFF) + mine * C::B_ROWS;
         const uint64_t pol_t = l2_policy(a.l2_t);
         const int row_bytes = a.K / 2;
         // rows 4 i + rr with even and odd i differ in bit 2 of the swizzle's row
         const uint32_t sw0 = (uint32_t)(rr * 128 + ((c ^ rr) << 4)), sw1 = (uint32_t)(rr * 128 + ((c ^ (rr + 4)) << 4));
-        int it = 0, s = 0;
-        uint32_t ph = 0;
+        int it = 0;
+        Ring st;
         bool ok = true;
         for (int L = first_tile; L < total && ok; L += tile_step) {
             int g, nt, row0, rows;
@@ -506,57 +575,58 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             __syncwarp();
             for (int kb = 0; kb < KB; ++kb, ++it) {
                 if (it % kGatherWarps == mine) {
-                    if (!wait(&ctl->empty[s], ph ^ 1u)) {
+                    if (!wait(&ctl->empty[st.i], st.ph ^ 1u)) {
                         ok = false;
                         break;
                     }
                     const int off = kb * (kStageK / 2) + c * 16;
                     const bool in = off < row_bytes;
                     const uint8_t* base = a.a_codes + (in ? off : 0);
-                    const uint32_t dst = smem_u32(opB(s));
+                    const uint32_t dst = smem_u32(opB(st.i));
 #pragma unroll 4
                     for (int i = 0; i < part / 4; i += 2) {
                         const int r0 = tab[4 * i + rr], r1 = tab[4 * i + 4 + rr];
                         cp_async16_p(dst + i * 512 + sw0, base + (size_t)max(r0, 0) * row_bytes, in && r0 >= 0 ? 16u : 0u, pol_t);
                         cp_async16_p(dst + i * 512 + 512 + sw1, base + (size_t)max(r1, 0) * row_bytes, in && r1 >= 0 ? 16u : 0u, pol_t);
                     }
-                    cp_async_arrive_noinc(&ctl->full[s]);
+                    cp_async_arrive_noinc(&mc->gfull[st.i]);
                 }
-                if (++s == C::STAGES) {
-                    s = 0;
-                    ph ^= 1u;
-                }
+                st.next(C::STAGES);
             }
         }
         cp_async_wait_all();
-        if (!ok && lane == 0) {
-            report_error(a.err, MOE_ERR_TIMEOUT, 7);
-            ctl->abort = 1;
-        }
+        if (!ok) give_up(7);
     }
 
+    // After an abort (PAIR: always; in a normal run these waits return at once) every role lets what
+    // it has in flight finish, so that no memory is released, or left by a CTA of the pair, in use.
     tc_fence_before();
     __syncthreads();
-    uint64_t* drain = warp >= 1 && warp < C::EPI_WARP0                          ? &ctl->drain[warp - 1]
-                      : warp >= C::SCALE_WARP0 && warp < C::GATHER_WARP0 ? &ctl->drain[C::NI + warp - C::SCALE_WARP0]
-                                                                         : nullptr;
-    if (PAIR) {
-        // Whether or not anything aborted, every CTA lets what it has in flight finish (in a normal
-        // run these waits return at once), so that neither's memory is in use by the other.
+    if (PAIR || *abort_flag) {
         int never = 0;
-        for (int q = 0; q < C::STAGES; ++q)
-            if (is.mask >> q & 1u) mbar_wait(&ctl->full[q], is.par >> q & 1u, &never);
+        const bool scale = warp >= C::SCALE_WARP0 && warp < C::GATHER_WARP0;
+        if (scale) {  // entry d is always the same warp's: its latest copy is the one to wait for
+            for (int d = 0; d < kSfRing; ++d)
+                if (is.mask >> d & 1u) mbar_wait(&mc->sf_ready[d], is.par >> d & 1u, &never);
+        } else if (warp == 0 && leader) {
+            for (int q = 0; q < C::STAGES; ++q)
+                if (is.mask >> q & 1u) mbar_wait(&ctl->full[q], is.par >> q & 1u, &never);
+        } else if (warp == 0 && is.mask && *abort_flag) {
+            // the peer's copies complete on the leader's barriers; those of a stage the leader never
+            // armed are not tracked: about 100 microseconds, far longer than a copy takes
+            const long long t0 = clock64();
+            while (clock64() - t0 < 200000) {
+            }
+        }
         if (is.tc) {
-            mma_commit_pair(drain, 0x1);
+            uint64_t* drain = &ctl->drain[warp - 1];
+            commit_here(drain);
             mbar_wait(drain, 0, &never);
         }
         tc_fence_before();
-        cluster_sync();
-    } else if (*abort_flag) {
-        drain_in_flight(is, ctl->full, C::STAGES, drain);
-        tc_fence_before();
-        __syncthreads();
     }
+    if (PAIR) cluster_sync();
+    else __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         if (PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
