@@ -81,6 +81,18 @@ MOE_DEV bool mbar_try_wait(uint32_t bar_addr, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// Whether that phase has completed, without waiting.
+MOE_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // Waits until the phase with the given parity has completed. Gives up after `limit`
 // cycles or when *abort becomes non-zero; returns false then.
 MOE_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, long long limit = kWaitLimitCycles) {

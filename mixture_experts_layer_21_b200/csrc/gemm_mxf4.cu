@@ -24,7 +24,7 @@
 // with one lane elected to issue:
 //   producer   the codes of both sides into the stages (tokens only in segment order)
 //   MMA        one issuer, or two with partial sums of their own
-//   copier     scale blocks from the scale ring into tensor-memory slots
+//   copiers    two: scale blocks from the scale ring into tensor-memory slots
 //   epilogue   four warps: tensor memory -> alpha, bf16 -> out
 //   scales     four warps, taking the stages in turn: both sides' scale blocks into the scale ring
 //   gather     four warps, likewise (with row_idx): the token rows' codes by cp.async
@@ -48,11 +48,17 @@ namespace {
 constexpr int kStageK = 256;
 constexpr int kScaleWarps = 4;
 constexpr int kGatherWarps = 4;
+constexpr int kCopiers = 1;
 constexpr int kSfRing = 8;
 
-// The control block with the barriers that only this kernel has.
+// Tiles whose rows the producer may have written and the MMA issuers not yet read: it is at most
+// kMaxStages stages, so at most as many tiles, ahead of the slowest of them.
+constexpr int kTileRing = 32;
+
+// The control block with what only this kernel has.
 struct Mxf4Ctl {
     CtrlBlock c;
+    int rows[kTileRing];  // rows of this CTA's tiles, written by the producer before the tile's first stage
     uint64_t gfull[kMaxStages], sf_ready[kSfRing], psf[kSfRing], sf_free[kSfRing], sf_full[kSfRing], slot_free[kSfRing];
 };
 
@@ -105,8 +111,8 @@ struct Mxf4Cfg {
     static constexpr int TAIL_BYTES = kSfRing * SF_ENTRY + STAGING_OFF + 4 * 2048;
     static constexpr int STAGES = cmin(kMaxStages, (kSmemLimit - 1024 - TAIL_BYTES) / STAGE);
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE + TAIL_BYTES;
-    static constexpr int COPIER_WARP = 1 + NI;
-    static constexpr int EPI_WARP0 = COPIER_WARP + 1;
+    static constexpr int COPIER_WARP0 = 1 + NI;
+    static constexpr int EPI_WARP0 = COPIER_WARP0 + kCopiers;
     static constexpr int SCALE_WARP0 = EPI_WARP0 + 4;
     static constexpr int GATHER_WARP0 = SCALE_WARP0 + kScaleWarps;
     static constexpr int THREADS = (GATHER_WARP0 + (GATHER ? kGatherWarps : 0)) * 32;
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             mbar_init(&ctl->tfull[b], C::NI);
             mbar_init(&ctl->tempty[b], PAIR ? 8 : 4);
         }
-        for (int i = 0; i <= C::NI; ++i) mbar_init(&ctl->drain[i], 1);
+        for (int i = 0; i < C::NI + kCopiers; ++i) mbar_init(&ctl->drain[i], 1);
         ctl->abort = 0;
         fence_barrier_init();
     }
@@ -249,8 +255,9 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
         const uint64_t pol_w = l2_policy(a.l2_w), pol_t = l2_policy(a.l2_t);
         constexpr uint32_t BYTES = C::A_BYTES + (GATHER ? 0 : C::B_BYTES);
         Ring st;
+        int n = 0;
         bool ok = true;
-        for (int L = first_tile; L < total && ok; L += tile_step) {
+        for (int L = first_tile; L < total && ok; L += tile_step, ++n) {
             int g, nt, row0, rows;
             tile(L, g, nt, row0, rows);
             const int wrow = (PAIR ? 2 * nt + rank : nt) * kTileN;  // a block past the last reads as zeros
@@ -262,6 +269,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                 }
                 const int s = st.i, x = kb * (kStageK / 2);
                 if (elect_one()) {
+                    if (kb == 0) mc->rows[n % kTileRing] = rows;  // the arrival below publishes it
                     if (PAIR) {
                         const uint32_t bar = mapa_shared(smem_u32(&ctl->full[s]), 0);  // the leader's
                         if (leader) mbar_arrive_expect_tx(&ctl->full[s], 2 * BYTES);
@@ -279,36 +287,43 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             }
         }
         if (!ok) give_up(1);
-    } else if (warp < C::COPIER_WARP) {
+    } else if (warp < C::COPIER_WARP0) {
         // ---------------- MMAs: issuer I takes its share of each stage's four K steps
         auto issue = [&](auto first) {
             constexpr int SHARE = 4 / C::NI, I = decltype(first)::value;
             const uint64_t a0 = sw128_kmajor_desc(smem_u32(opA(0))), b0 = sw128_kmajor_desc(smem_u32(opB(0)));
+            constexpr uint32_t id2 = idesc_mxf4(0, 0, 2) ^ idesc_mxf4(0, 0, 0), at2 = 2u << 30;
             Ring st, sl;
-            int b = 0;
-            uint32_t bph = 0;
-            bool ok = true;
-            for (int L = first_tile; L < total && ok; L += tile_step) {
-                int g, nt, row0, rows;
-                tile(L, g, nt, row0, rows);
-                const uint32_t idesc = idesc_mxf4(PAIR ? 2 * kTileN : kTileN, mma_n(rows), 0);
-                constexpr uint32_t id2 = idesc_mxf4(0, 0, 2) ^ idesc_mxf4(0, 0, 0), at2 = 2u << 30;
+            int b = 0, n = 0;
+            uint32_t bph = 0, idesc = 0;
+            bool ok = true, next_sf = false, next_full = false, next_g = !GATHER;
+            for (int L = first_tile; L < total && ok; L += tile_step, ++n) {
                 if (!wait(&ctl->tempty[b], bph ^ 1u)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)((b * C::NI + I) * BT);
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!wait(&mc->sf_full[sl.i], sl.ph) || !wait(&ctl->full[st.i], st.ph) ||
-                        (GATHER && !wait(&mc->gfull[st.i], st.ph)) || (GATHER && PAIR && !wait(&pfull[st.i], st.ph))) {
+                    if ((!next_sf && !wait(&mc->sf_full[sl.i], sl.ph)) || (!next_full && !wait(&ctl->full[st.i], st.ph)) ||
+                        (!next_g && !wait(&mc->gfull[st.i], st.ph)) ||
+                        (GATHER && PAIR && !wait(&pfull[st.i], st.ph))) {
                         ok = false;
                         break;
                     }
                     if (GATHER) fence_proxy_async_smem();  // the gathered rows came by the generic proxy
                     tc_fence_after();
-                    const uint64_t as = a0 + (uint64_t)(st.i * (C::STAGE >> 4)), bs = b0 + (uint64_t)(st.i * (C::STAGE >> 4));
-                    const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + sl.i * C::SF_SLOT);
+                    if (kb == 0)
+                        idesc = idesc_mxf4(PAIR ? 2 * kTileN : kTileN,
+                                           mma_n(__shfl_sync(0xffffffffu, mc->rows[n % kTileRing], 0)), 0);
+                    const int s = st.i, t = sl.i;
+                    st.next(C::STAGES);
+                    sl.next(C::SLOTS);
+                    // a look at the next stage's barriers, whose answers come while the MMAs are issued
+                    next_sf = mbar_test(&mc->sf_full[sl.i], sl.ph);
+                    next_full = mbar_test(&ctl->full[st.i], st.ph);
+                    if (GATHER) next_g = mbar_test(&mc->gfull[st.i], st.ph);
+                    const uint64_t as = a0 + (uint64_t)(s * (C::STAGE >> 4)), bs = b0 + (uint64_t)(s * (C::STAGE >> 4));
+                    const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + t * C::SF_SLOT);
                     const int steps = (a.K - kb * kStageK + 63) >> 6;
                     if (elect_one()) {
 #pragma unroll
@@ -323,11 +338,12 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                             }
                         }
                         is.tc = true;
-                        commit(&ctl->empty[st.i]);
-                        commit_here(&mc->slot_free[sl.i]);
+                        commit(&ctl->empty[s]);
+                        commit_here(&mc->slot_free[t]);
                     }
-                    st.next(C::STAGES);
-                    sl.next(C::SLOTS);
+                    next_sf = __all_sync(0xffffffffu, next_sf);
+                    next_full = __all_sync(0xffffffffu, next_full);
+                    if (GATHER) next_g = __all_sync(0xffffffffu, next_g);
                 }
                 if (!ok) break;
                 if (elect_one()) commit(&ctl->tfull[b]);
@@ -357,40 +373,49 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             }
             if (!ok) give_up(6);
         }
-    } else if (warp == C::COPIER_WARP) {
-        // ---------------- scale blocks: ring -> tensor memory (peer: tells the leader they are in its ring)
+    } else if (warp < C::EPI_WARP0) {
+        // ---------------- scale blocks: ring -> tensor memory (peer: tells the leader they are in its
+        // ring); the copiers take the stages in turn
+        const uint64_t ring0 = sf_block_desc(smem_u32(sf_ring));
+        const int mine = warp - C::COPIER_WARP0;
+        int it = 0;
         Ring rg, sl;
         bool ok = true;
         for (int L = first_tile; L < total && ok; L += tile_step) {
-            for (int kb = 0; kb < KB; ++kb) {
-                if (!wait(&mc->sf_ready[rg.i], rg.ph) ||
-                    (leader && ((PAIR && !wait(&mc->psf[rg.i], rg.ph)) || !wait(&mc->slot_free[sl.i], sl.ph ^ 1u)))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (elect_one()) {
-                    if (!leader) {
-                        mbar_arrive_remote(mapa_shared(smem_u32(&mc->psf[rg.i]), 0));
-                    } else {
-                        const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + sl.i * C::SF_SLOT), sfb = sfa + 8;
-                        const int halves = min(2, a.KS - 2 * kb);
-                        auto copy = [](uint32_t t, uint64_t desc) {
-                            if (PAIR) tmem_cp_32x128b_x4_pair(t, desc);
-                            else tmem_cp_32x128b_x4(t, desc);
-                        };
+            int g, nt, row0, rows;
+            tile(L, g, nt, row0, rows);
+            const bool wide = C::RG > 1 && mma_n(rows) > 128;  // the second 128-row group is in use
+            for (int kb = 0; kb < KB; ++kb, ++it) {
+                if (it % kCopiers == mine) {
+                    if (!wait(&mc->sf_ready[rg.i], rg.ph) ||
+                        (leader && ((PAIR && !wait(&mc->psf[rg.i], rg.ph)) || !wait(&mc->slot_free[sl.i], sl.ph ^ 1u)))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t src = ring0 + (uint64_t)(rg.i * (C::SF_ENTRY >> 4));
+                    const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + sl.i * C::SF_SLOT), sfb = sfa + 8;
+                    const bool both = a.KS - 2 * kb > 1;  // both 128-K halves
+                    auto copy = [](uint32_t t, uint64_t desc) {
+                        if (PAIR) tmem_cp_32x128b_x4_pair(t, desc);
+                        else tmem_cp_32x128b_x4(t, desc);
+                    };
+                    if (elect_one()) {
+                        if (!leader) {
+                            mbar_arrive_remote(mapa_shared(smem_u32(&mc->psf[rg.i]), 0));
+                        } else {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (h < halves) {
-                                copy(sfa + 4 * h, sf_block_desc(smem_u32(sfA(rg.i)) + 512 * h));
-#pragma unroll
-                                for (int r = 0; r < C::RG; ++r)
-                                    copy(sfb + 4 * (h * C::RG + r), sf_block_desc(smem_u32(sfB(rg.i, h, r))));
+                            for (int h = 0; h < 2; ++h) {
+                                if (h == 0 || both) {
+                                    copy(sfa + 4 * h, src + 32 * h);
+                                    copy(sfb + 4 * h * C::RG, src + 64 + 32 * h * C::RG);
+                                    if (wide) copy(sfb + 4 * (h * C::RG + 1), src + 64 + 32 * (h * C::RG + 1));
+                                }
                             }
+                            is.tc = true;
+                            commit_here(&mc->sf_full[sl.i]);
+                            commit(&mc->sf_free[rg.i]);
                         }
-                        is.tc = true;
-                        commit_here(&mc->sf_full[sl.i]);
-                        commit(&mc->sf_free[rg.i]);
                     }
                 }
                 rg.next(kSfRing);
