@@ -728,19 +728,26 @@ cudaError_t launch_gemm_mxf4(const Mxf4Problem& p, cudaStream_t st, bool pdl) {
     l2_policies(&a.l2_w, &a.l2_t);
     CUtensorMap tw;
     if (!make_map_codes(&tw, p.kdata, (uint64_t)Kp / 2, p.N, p.G)) return cudaErrorInvalidValue;
+    // Token tile: a tile costs a stage per 256 K whatever its width, so it should hold a whole segment;
+    // mean + 2 sqrt(mean) covers nearly every one. Longer segments go to CTA pairs, where there is a
+    // tile for each pair of SMs: 8 experts x 14336 x 4096 with 128 rows each took 56 us on pairs, 59 in
+    // 128-token tiles (62 and 73 gathered), with 1024 rows 246 and 295; with 64 rows 53 and 49.
+    // MOE_TOKEN_TILE=16|32|64|128 and MOE_GEMM_PAIRS=0|1 override the choice (tests, tuning).
     const long long segs = std::max<long long>(1, std::min<long long>(p.G, p.M_alloc));
     const double avg = (double)p.M_alloc / (double)segs;
-    // MOE_TOKEN_TILE=16|32|64|128|192 overrides the token-tile choice (tests, tuning)
     const char* env = getenv("MOE_TOKEN_TILE");
     const int v = env ? atoi(env) : 0;
-    const double want = v == 16 || v == 32 || v == 64 || v == 128 || v == 192 ? v : avg + 2.0 * std::sqrt(avg);
+    const bool forced = v == 16 || v == 32 || v == 64 || v == 128;
+    const double want = forced ? v : avg + 2.0 * std::sqrt(avg);
+    const char* pe = getenv("MOE_GEMM_PAIRS");
+    const int mode = pe && (pe[0] == '0' || pe[0] == '1') && pe[1] == '\0' ? pe[0] - '0' : 2;
+    const long long pair_tiles = ((long long)p.M_alloc + 191) / 192 * ((a.NT1 + 1) / 2);
+    if (mode == 1 || (mode == 2 && want > 128 && pair_tiles >= num_sms() / 2))
+        return run_mxf4_bt<192, true>(p, tw, a, st, pdl);
     if (want <= 16) return run_mxf4_bt<16>(p, tw, a, st, pdl);
     if (want <= 32) return run_mxf4_bt<32>(p, tw, a, st, pdl);
     if (want <= 64) return run_mxf4_bt<64>(p, tw, a, st, pdl);
-    const char* pe = getenv("MOE_GEMM_PAIRS");
-    if (pe && pe[0] == '1') return run_mxf4_bt<192, true>(p, tw, a, st, pdl);
-    if (want <= 128) return run_mxf4_bt<128>(p, tw, a, st, pdl);
-    return run_mxf4_bt<192>(p, tw, a, st, pdl);
+    return run_mxf4_bt<128>(p, tw, a, st, pdl);
 }
 
 }  // namespace moe
