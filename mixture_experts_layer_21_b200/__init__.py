@@ -157,21 +157,26 @@ def _check(status: int, where: str) -> None:
 
 def _launch_stream(dev: torch.device, stream) -> int:
     """The stream of a call on `dev`'s tensors; the kernels run on the current device."""
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+    if dev.type != "cuda" or dev.index != torch._C._cuda_getDevice():
         raise ValueError(f"need tensors on the current CUDA device, got {dev}")
-    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
 
 
-def _want(t, name: str, shape, dtype, dev: torch.device, dense: bool = True) -> None:
-    """A tensor argument of this shape and type on this device; rows contiguous, and dense unless
-    the call takes a row stride."""
-    if t.shape != shape or t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)) or t.device != dev:
-        raise ValueError(f"{name}: need {tuple(shape)} {dtype} on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
-    if dense:
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: need a contiguous tensor, got strides {t.stride()}")
-    elif t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: need contiguous rows that do not overlap, got strides {t.stride()}")
+def _want(t, name: str, shape, dtypes, dev: torch.device, dense: bool = True) -> None:
+    """A tensor argument of this shape and one of these types on this device; rows contiguous, and
+    dense unless the call takes a row stride."""
+    if t.shape == shape and t.dtype in dtypes and t.device == dev:
+        if t.is_contiguous():
+            return
+        if not dense and (t.shape[1] <= 1 or t.stride(1) == 1) and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1]):
+            return
+        raise ValueError(f"{name}: need {'a contiguous tensor' if dense else 'contiguous rows that do not overlap'}, "
+                         f"got strides {t.stride()}")
+    raise ValueError(f"{name}: need {tuple(shape)} {dtypes} on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+_F32, _BF16, _I32, _U8 = (torch.float32,), (torch.bfloat16,), (torch.int32,), (torch.uint8,)
+_F32_BF16 = (torch.float32, torch.bfloat16)
 
 
 def _row_stride(t: torch.Tensor) -> int:
@@ -273,17 +278,17 @@ def moe_route_scored(logits: torch.Tensor, topk: int, scoring: str = "softmax", 
     T, E = logits.shape
     dev = logits.device
     st = _launch_stream(dev, stream)
-    _want(logits, "logits", (T, E), (torch.float32, torch.bfloat16), dev, dense=False)
+    _want(logits, "logits", (T, E), _F32_BF16, dev, dense=False)
     if bias is not None:
-        _want(bias, "bias", (E,), torch.float32, dev)
+        _want(bias, "bias", (E,), _F32, dev)
     if ids is None:
         ids = torch.empty(T, topk, dtype=torch.int32, device=dev)
     else:
-        _want(ids, "ids", (T, topk), torch.int32, dev)
+        _want(ids, "ids", (T, topk), _I32, dev)
     if w is None:
         w = torch.empty(T, topk, dtype=torch.float32, device=dev)
     else:
-        _want(w, "w", (T, topk), torch.float32, dev)
+        _want(w, "w", (T, topk), _F32, dev)
     _check(_lib.moe_route_scored(_ptr(logits), logits.dtype == torch.bfloat16, _row_stride(logits), _ptr(bias), T, E,
                                  topk, SCORING[scoring], n_group, topk_group, GROUP_SCORE[group_score], renormalize,
                                  routed_scaling_factor, _ptr(ids), _ptr(w), st), "moe_route_scored")
@@ -305,11 +310,11 @@ def moe_add_rmsnorm(x: torch.Tensor, weight=None, residual=None, eps: float = 1e
     st = _launch_stream(dev, stream)
     out = out or {}
     bf16 = torch.bfloat16
-    _want(x, "x", (T, H), (torch.float32, bf16), dev, dense=False)
+    _want(x, "x", (T, H), _F32_BF16, dev, dense=False)
     if residual is not None:
-        _want(residual, "residual", (T, H), bf16, dev, dense=False)
+        _want(residual, "residual", (T, H), _BF16, dev, dense=False)
     if weight is not None:
-        _want(weight, "weight", (H,), (torch.float32, bf16), dev)
+        _want(weight, "weight", (H,), _F32_BF16, dev)
     if deq and quant is None:
         raise ValueError("deq needs quant")
 
@@ -319,7 +324,7 @@ def moe_add_rmsnorm(x: torch.Tensor, weight=None, residual=None, eps: float = 1e
         t = out.get(name)
         if t is None:
             return torch.empty(shape, dtype=dtype, device=dev)
-        _want(t, name, shape, dtype, dev, dense)
+        _want(t, name, shape, (dtype,), dev, dense)
         return t
 
     r = buf("residual", residual is not None, (T, H), bf16, dense=False)
@@ -405,20 +410,19 @@ def moe_grouped_gemm_mxfp4(a_codes: torch.Tensor, a_scales: torch.Tensor, w: Wei
     permutation's perm_token); without it the R rows are in segment order. bf16 out [M,N]."""
     R, dev = a_codes.shape[0], a_codes.device
     st = _launch_stream(dev, stream)
-    u8 = torch.uint8
-    _want(a_codes, "a_codes", (R, w.K // 2), u8, dev)
-    _want(a_scales, "a_scales", (R, w.K // 32), u8, dev)
-    _want(cu_seqlens, "cu_seqlens", (w.G,), torch.int32, dev)
+    _want(a_codes, "a_codes", (R, w.K // 2), _U8, dev)
+    _want(a_scales, "a_scales", (R, w.K // 32), _U8, dev)
+    _want(cu_seqlens, "cu_seqlens", (w.G,), _I32, dev)
     M = R
     if row_idx is not None:
         M = row_idx.shape[0]
-        _want(row_idx, "row_idx", (M,), torch.int32, dev)
+        _want(row_idx, "row_idx", (M,), _I32, dev)
     if out is None:
         out = torch.empty(M, w.N, dtype=torch.bfloat16, device=dev)
     else:
-        _want(out, "out", (M, w.N), torch.bfloat16, dev)
+        _want(out, "out", (M, w.N), _BF16, dev)
     if ws is None:
-        ws = torch.zeros(256, dtype=u8, device=dev)
+        ws = torch.zeros(256, dtype=torch.uint8, device=dev)
     _check(_lib.moe_grouped_gemm_mxfp4(_ptr(a_codes), _ptr(a_scales), R, _ptr(row_idx), M, ctypes.byref(w.desc),
                                        _ptr(cu_seqlens), _ptr(out), _ptr(ws), ws.numel(), st), "moe_grouped_gemm_mxfp4")
     return out
@@ -499,13 +503,13 @@ def moe_quantize_mxfp4(x: torch.Tensor, deq: bool = False, out=None, stream=None
     dev = x.device
     st = _launch_stream(dev, stream)
     out = out or {}
-    _want(x, "x", (R, K), (torch.float32, torch.bfloat16), dev, dense=False)
+    _want(x, "x", (R, K), _F32_BF16, dev, dense=False)
 
     def buf(name, shape, dtype):
         t = out.get(name)
         if t is None:
             return torch.empty(shape, dtype=dtype, device=dev)
-        _want(t, name, shape, dtype, dev)
+        _want(t, name, shape, (dtype,), dev)
         return t
 
     codes = buf("codes", (R, K // 2), torch.uint8)

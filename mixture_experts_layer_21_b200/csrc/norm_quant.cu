@@ -120,24 +120,35 @@ MOE_DEV void quantize_chunk(const float (&v)[8], bool live, size_t c, uint8_t* c
     }
 }
 
-// One thread per eight values, rows in any stride.
-template <bool F32>
+// Each thread takes kQuantUnroll chunks of eight values, a block's width apart, all loaded before the
+// first is used. DENSE: the rows follow one another, and a chunk's place needs no division.
+constexpr int kQuantUnroll = 4;
+template <bool F32, bool DENSE>
 __global__ void __launch_bounds__(256) quant_mxfp4_kernel(const void* in, long long stride, int R, int K, uint8_t* codes,
                                                           uint8_t* scales, __nv_bfloat16* deq) {
     pdl_wait();
     const int per_row = K / 8;
     const long long n = (long long)R * per_row;
-    const long long step = (long long)gridDim.x * blockDim.x;
-    const long long first = blockIdx.x * (long long)blockDim.x + (threadIdx.x & ~31);
-    for (long long c0 = first; c0 < n; c0 += step) {  // the same trip count in every lane of a warp
-        const long long c = c0 + lane_id();
-        const bool live = c < n;
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (live) {
-            const long long r = c / per_row;
-            load_chunk<F32>(in, (size_t)r * stride + (size_t)(c - r * per_row) * 8, v);
+    const long long c0 = (long long)blockIdx.x * (256 * kQuantUnroll) + threadIdx.x;
+    float v[kQuantUnroll][8];
+#pragma unroll
+    for (int u = 0; u < kQuantUnroll; ++u) {
+        const long long c = c0 + u * 256;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[u][j] = 0.0f;
+        if (c < n) {
+            size_t off = (size_t)c * 8;
+            if (!DENSE) {
+                const long long r = c / per_row;
+                off = (size_t)r * stride + (size_t)(c - r * per_row) * 8;
+            }
+            load_chunk<F32>(in, off, v[u]);
         }
-        quantize_chunk<MOE_Q_MXFP4>(v, live, (size_t)c, codes, scales, deq);
+    }
+#pragma unroll
+    for (int u = 0; u < kQuantUnroll; ++u) {
+        const long long c = c0 + u * 256;
+        quantize_chunk<MOE_Q_MXFP4>(v[u], c < n, (size_t)c, codes, scales, deq);
     }
     pdl_launch();
 }
@@ -210,16 +221,27 @@ cudaError_t run_rmsnorm(const moe_rmsnorm_args_t& a, int threads, cudaStream_t s
 
 cudaError_t launch_quant_mxfp4(const void* in, bool in_f32, long long stride, int R, int K, uint8_t* codes,
                                uint8_t* scales, void* deq, cudaStream_t st, bool pdl) {
-    const long long n = (long long)R * (K / 8);
-    const unsigned blocks = (unsigned)std::min<long long>((n + 255) / 256, (long long)num_sms() * 32);
+    const long long n = (long long)R * (K / 8), per_block = 256 * kQuantUnroll;
+    const long long blocks = (n + per_block - 1) / per_block;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     __nv_bfloat16* d = static_cast<__nv_bfloat16*>(deq);
-    if (in_f32) return launch_k(quant_mxfp4_kernel<true>, dim3(blocks), dim3(256), 0, st, pdl, in, stride, R, K, codes, scales, d);
-    return launch_k(quant_mxfp4_kernel<false>, dim3(blocks), dim3(256), 0, st, pdl, in, stride, R, K, codes, scales, d);
+    const dim3 grid((unsigned)blocks), block(256);
+    const bool dense = stride == K || R == 1;
+    if (in_f32) {
+        if (dense) return launch_k(quant_mxfp4_kernel<true, true>, grid, block, 0, st, pdl, in, stride, R, K, codes, scales, d);
+        return launch_k(quant_mxfp4_kernel<true, false>, grid, block, 0, st, pdl, in, stride, R, K, codes, scales, d);
+    }
+    if (dense) return launch_k(quant_mxfp4_kernel<false, true>, grid, block, 0, st, pdl, in, stride, R, K, codes, scales, d);
+    return launch_k(quant_mxfp4_kernel<false, false>, grid, block, 0, st, pdl, in, stride, R, K, codes, scales, d);
 }
 
 cudaError_t launch_add_rmsnorm(const moe_rmsnorm_args_t& a, cudaStream_t st, bool pdl) {
+    // Few rows: a row is spread as thin as it goes, for the shortest way through it. Many: four chunks a
+    // thread, so that more rows are in flight on an SM between their barriers.
     const int chunks = a.H / 8;
-    const int cpt = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
+    const bool many = a.T >= 2 * num_sms();
+    const char* ce = getenv("CPT");
+    const int cpt = ce ? atoi(ce) : chunks > 2048 || (many && chunks >= 256) ? 4 : chunks > 1024 || (many && chunks >= 128) ? 2 : 1;
     const int threads = ((chunks + cpt - 1) / cpt + 31) / 32 * 32;
     if (a.x_is_f32) {
         if (cpt == 1) return run_rmsnorm<1, true>(a, threads, st, pdl);
