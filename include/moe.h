@@ -158,9 +158,21 @@ moe_status_t moe_route_topk_grouped(const float* logits, const float* bias, int 
  */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
 typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score_t;
-moe_status_t moe_route_scored(const void* logits, int in_is_bf16, int64_t row_stride, const float* bias, int T, int E,
-                              int topk, int scoring, int n_group, int topk_group, int group_score, int renormalize,
-                              float routed_scaling_factor, int32_t* topk_ids, float* topk_w, moe_stream_t stream);
+typedef struct {
+    const void* logits;
+    const float* bias;              /* or NULL */
+    int32_t* topk_ids;
+    float* topk_w;
+    int64_t row_stride;
+    int32_t in_is_bf16;
+    int32_t T, E, topk;
+    int32_t scoring;                /* moe_score_t */
+    int32_t n_group, topk_group;
+    int32_t group_score;            /* moe_group_score_t */
+    int32_t renormalize;
+    float routed_scaling_factor;
+} moe_route_args_t;
+moe_status_t moe_route_scored(const moe_route_args_t* args, moe_stream_t stream);
 
 /*
  * What stands before the layer — residual addition and root-mean-square norm of rows, in one

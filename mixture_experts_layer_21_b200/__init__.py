@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass, field
 
 import torch
@@ -79,6 +80,20 @@ class moe_rmsnorm_args_t(ctypes.Structure):
                 ("deq", ctypes.c_void_p)]
 
 
+class moe_route_args_t(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("topk_ids", ctypes.c_void_p),
+                ("topk_w", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("in_is_bf16", ctypes.c_int32),
+                ("T", ctypes.c_int32), ("E", ctypes.c_int32), ("topk", ctypes.c_int32), ("scoring", ctypes.c_int32),
+                ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("routed_scaling_factor", ctypes.c_float)]
+
+
+# The two argument structures in one pack each, a fraction of the time that a ctypes object takes to
+# fill: what a one-token call spends on the host is most of its time.
+_ROUTE_ARGS = struct.Struct("PPPPqiiiiiiiiif")
+_RMSNORM_ARGS = struct.Struct("PPPiiiiqqqqfiPPPPP")
+
+
 class moe_forward_args_t(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("router_logits", ctypes.c_void_p),
                 ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32),
@@ -127,8 +142,8 @@ _sig = {
     "moe_route_topk_grouped": (_I, [_P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P]),
     "moe_bias_act_and_mul": (_I, [_P, _P, _I, _P, _P, _P, _I, _P, _I, _I, ctypes.POINTER(moe_act_ex_t), _P, _P]),
     "moe_forward_workspace_size_args": (_S, [ctypes.POINTER(moe_forward_args_t)]),
-    "moe_route_scored": (_I, [_P, _I, _L, _P, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P]),
-    "moe_add_rmsnorm": (_I, [ctypes.POINTER(moe_rmsnorm_args_t), _P]),
+    "moe_route_scored": (_I, [_P, _P]),      # moe_route_args_t*
+    "moe_add_rmsnorm": (_I, [_P, _P]),       # moe_rmsnorm_args_t*
     "moe_quantize_mxfp4": (_I, [_P, _I, _L, _I, _I, _P, _P, _P, _P]),
     "moe_grouped_gemm_mxfp4": (_I, [_P, _P, _I, _P, _I, ctypes.POINTER(moe_weight_t), _P, _P, _P, _S, _P]),
 }
@@ -155,33 +170,41 @@ def _check(status: int, where: str) -> None:
         raise MoEError(status, where)
 
 
-def _launch_stream(dev: torch.device, stream) -> int:
-    """The stream of a call on `dev`'s tensors; the kernels run on the current device."""
-    if dev.type != "cuda" or dev.index != torch._C._cuda_getDevice():
-        raise ValueError(f"need tensors on the current CUDA device, got {dev}")
-    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+def _launch_device(t: torch.Tensor) -> int:
+    """The device of a call, that of its first tensor: the kernels run on the current device."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"need tensors on the current CUDA device, got {t.device}")
+    return dev
 
 
-def _want(t, name: str, shape, dtypes, dev: torch.device, dense: bool = True) -> None:
-    """A tensor argument of this shape and one of these types on this device; rows contiguous, and
-    dense unless the call takes a row stride."""
-    if t.shape == shape and t.dtype in dtypes and t.device == dev:
+def _launch_stream(dev: int, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _want(t, name: str, shape, dtype, dev: int, dense: bool = True) -> None:
+    """A tensor argument of this shape and type on this device; rows contiguous, and dense unless the
+    call takes a row stride."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
         if t.is_contiguous():
             return
         if not dense and (t.shape[1] <= 1 or t.stride(1) == 1) and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1]):
             return
         raise ValueError(f"{name}: need {'a contiguous tensor' if dense else 'contiguous rows that do not overlap'}, "
                          f"got strides {t.stride()}")
-    raise ValueError(f"{name}: need {tuple(shape)} {dtypes} on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    raise ValueError(f"{name}: need {tuple(shape)} {dtype} on cuda:{dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
-_F32, _BF16, _I32, _U8 = (torch.float32,), (torch.bfloat16,), (torch.int32,), (torch.uint8,)
-_F32_BF16 = (torch.float32, torch.bfloat16)
+def _float_type(t, name: str) -> torch.dtype:
+    if t.dtype is torch.bfloat16 or t.dtype is torch.float32:
+        return t.dtype
+    raise ValueError(f"{name}: need bf16 or fp32, got {t.dtype}")
 
 
 def _row_stride(t: torch.Tensor) -> int:
     """Elements between rows (a single row's stride is not used)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    rows, cols = t.shape
+    return cols if rows <= 1 or t.is_contiguous() else t.stride(0)
 
 
 def version() -> str:
@@ -215,6 +238,10 @@ class Weight:
         d.G, d.N = self.data.shape[0], self.data.shape[1]
         d.K = self.data.shape[2] * (1 if self.fmt == "bf16" else 2)
         d.data, d.scale, d.alpha = _ptr(self.data), _ptr(self.scale), _ptr(self.alpha)
+
+    @property
+    def desc_ref(self):
+        return ctypes.byref(self.desc)
 
     @property
     def G(self):
@@ -276,22 +303,23 @@ def moe_route_scored(logits: torch.Tensor, topk: int, scoring: str = "softmax", 
     best ("max") or two best ("top2") experts, and raw or renormalised weights. logits fp32 or bf16
     [T,E], rows in any stride; a logit of -inf masks its expert."""
     T, E = logits.shape
-    dev = logits.device
-    st = _launch_stream(dev, stream)
-    _want(logits, "logits", (T, E), _F32_BF16, dev, dense=False)
+    dev = _launch_device(logits)
+    dt = _float_type(logits, "logits")
+    _want(logits, "logits", (T, E), dt, dev, dense=False)
     if bias is not None:
-        _want(bias, "bias", (E,), _F32, dev)
+        _want(bias, "bias", (E,), torch.float32, dev)
     if ids is None:
-        ids = torch.empty(T, topk, dtype=torch.int32, device=dev)
+        ids = torch.empty(T, topk, dtype=torch.int32, device=logits.device)
     else:
-        _want(ids, "ids", (T, topk), _I32, dev)
+        _want(ids, "ids", (T, topk), torch.int32, dev)
     if w is None:
-        w = torch.empty(T, topk, dtype=torch.float32, device=dev)
+        w = torch.empty(T, topk, dtype=torch.float32, device=logits.device)
     else:
-        _want(w, "w", (T, topk), _F32, dev)
-    _check(_lib.moe_route_scored(_ptr(logits), logits.dtype == torch.bfloat16, _row_stride(logits), _ptr(bias), T, E,
-                                 topk, SCORING[scoring], n_group, topk_group, GROUP_SCORE[group_score], renormalize,
-                                 routed_scaling_factor, _ptr(ids), _ptr(w), st), "moe_route_scored")
+        _want(w, "w", (T, topk), torch.float32, dev)
+    a = _ROUTE_ARGS.pack(logits.data_ptr(), 0 if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr(),
+                         _row_stride(logits), dt is torch.bfloat16, T, E, topk, SCORING[scoring], n_group, topk_group,
+                         GROUP_SCORE[group_score], renormalize, routed_scaling_factor)
+    _check(_lib.moe_route_scored(a, _launch_stream(dev, stream)), "moe_route_scored")
     return ids, w
 
 
@@ -306,38 +334,39 @@ def moe_add_rmsnorm(x: torch.Tensor, weight=None, residual=None, eps: float = 1e
     rows of r) comes with a residual, ``y`` (bf16) with want_y, ``codes`` and ``scales`` with quant,
     ``deq`` (bf16, the values they stand for) with deq."""
     T, H = x.shape
-    dev = x.device
-    st = _launch_stream(dev, stream)
+    dev = _launch_device(x)
     out = out or {}
-    bf16 = torch.bfloat16
-    _want(x, "x", (T, H), _F32_BF16, dev, dense=False)
+    bf16, u8, shape = torch.bfloat16, torch.uint8, (T, H)
+    xt = _float_type(x, "x")
+    _want(x, "x", shape, xt, dev, dense=False)
     if residual is not None:
-        _want(residual, "residual", (T, H), _BF16, dev, dense=False)
+        _want(residual, "residual", shape, bf16, dev, dense=False)
     if weight is not None:
-        _want(weight, "weight", (H,), _F32_BF16, dev)
+        _want(weight, "weight", (H,), _float_type(weight, "weight"), dev)
     if deq and quant is None:
         raise ValueError("deq needs quant")
 
-    def buf(name, wanted, shape, dtype, dense=True):
-        if not wanted:
-            return None
+    def buf(name, shape, dtype, dense):
         t = out.get(name)
         if t is None:
-            return torch.empty(shape, dtype=dtype, device=dev)
-        _want(t, name, shape, (dtype,), dev, dense)
+            return torch.empty(shape, dtype=dtype, device=x.device)
+        _want(t, name, shape, dtype, dev, dense)
         return t
 
-    r = buf("residual", residual is not None, (T, H), bf16, dense=False)
-    y = buf("y", want_y, (T, H), bf16, dense=False)
-    codes = buf("codes", quant is not None, (T, H // 2 if quant == "mxfp4" else H), torch.uint8)
-    scales = buf("scales", quant is not None, (T, H // 32), torch.uint8)
-    d = buf("deq", deq, (T, H), bf16)
-    a = moe_rmsnorm_args_t(_ptr(x), _ptr(residual), _ptr(weight), x.dtype != bf16,
-                           weight is not None and weight.dtype != bf16, T, H, _row_stride(x),
+    r = None if residual is None else buf("residual", shape, bf16, False)
+    y = buf("y", shape, bf16, False) if want_y else None
+    codes = scales = d = None
+    if quant is not None:
+        codes = buf("codes", (T, H // 2) if quant == "mxfp4" else shape, u8, True)
+        scales = buf("scales", (T, H // 32), u8, True)
+        if deq:
+            d = buf("deq", shape, bf16, True)
+    p = lambda t: 0 if t is None else t.data_ptr()
+    a = _RMSNORM_ARGS.pack(x.data_ptr(), p(residual), p(weight), xt is not bf16,
+                           weight is not None and weight.dtype is not bf16, T, H, _row_stride(x),
                            0 if residual is None else _row_stride(residual), 0 if r is None else _row_stride(r),
-                           0 if y is None else _row_stride(y), eps, QUANT[quant], _ptr(r), _ptr(y), _ptr(codes),
-                           _ptr(scales), _ptr(d))
-    _check(_lib.moe_add_rmsnorm(ctypes.byref(a), st), "moe_add_rmsnorm")
+                           0 if y is None else _row_stride(y), eps, QUANT[quant], p(r), p(y), p(codes), p(scales), p(d))
+    _check(_lib.moe_add_rmsnorm(a, _launch_stream(dev, stream)), "moe_add_rmsnorm")
     return dict(residual=r, y=y, codes=codes, scales=scales, deq=d)
 
 
@@ -408,23 +437,28 @@ def moe_grouped_gemm_mxfp4(a_codes: torch.Tensor, a_scales: torch.Tensor, w: Wei
     """Block-scaled grouped GEMM on MXFP4 activations (codes [R,K/2], e8m0 scales [R,K/32]) and
     prepared MXFP4 weights. row_idx (int32 [M]): row r of the segments is row row_idx[r] of a (the
     permutation's perm_token); without it the R rows are in segment order. bf16 out [M,N]."""
-    R, dev = a_codes.shape[0], a_codes.device
-    st = _launch_stream(dev, stream)
-    _want(a_codes, "a_codes", (R, w.K // 2), _U8, dev)
-    _want(a_scales, "a_scales", (R, w.K // 32), _U8, dev)
-    _want(cu_seqlens, "cu_seqlens", (w.G,), _I32, dev)
+    R, dev, u8 = a_codes.shape[0], _launch_device(a_codes), torch.uint8
+    K, N = w.K, w.N
+    _want(a_codes, "a_codes", (R, K // 2), u8, dev)
+    _want(a_scales, "a_scales", (R, K // 32), u8, dev)
+    _want(cu_seqlens, "cu_seqlens", (w.G,), torch.int32, dev)
+    if w.data.get_device() != dev:
+        raise ValueError(f"w: need weights on cuda:{dev}, got {w.data.device}")
     M = R
     if row_idx is not None:
         M = row_idx.shape[0]
-        _want(row_idx, "row_idx", (M,), _I32, dev)
+        _want(row_idx, "row_idx", (M,), torch.int32, dev)
     if out is None:
-        out = torch.empty(M, w.N, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=a_codes.device)
     else:
-        _want(out, "out", (M, w.N), _BF16, dev)
+        _want(out, "out", (M, N), torch.bfloat16, dev)
     if ws is None:
-        ws = torch.zeros(256, dtype=torch.uint8, device=dev)
-    _check(_lib.moe_grouped_gemm_mxfp4(_ptr(a_codes), _ptr(a_scales), R, _ptr(row_idx), M, ctypes.byref(w.desc),
-                                       _ptr(cu_seqlens), _ptr(out), _ptr(ws), ws.numel(), st), "moe_grouped_gemm_mxfp4")
+        ws = torch.zeros(256, dtype=u8, device=a_codes.device)
+    elif ws.get_device() != dev:
+        raise ValueError(f"ws: need a workspace on cuda:{dev}, got {ws.device}")
+    _check(_lib.moe_grouped_gemm_mxfp4(a_codes.data_ptr(), a_scales.data_ptr(), R, _ptr(row_idx), M, w.desc_ref,
+                                       cu_seqlens.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                       _launch_stream(dev, stream)), "moe_grouped_gemm_mxfp4")
     return out
 
 
@@ -500,23 +534,23 @@ def moe_quantize_mxfp4(x: torch.Tensor, deq: bool = False, out=None, stream=None
     e8m0 scales [R,K/32] and, with deq, the bf16 values they stand for [R,K] (else None). ``out``:
     optional dict of caller-allocated outputs (any of codes, scales, deq)."""
     R, K = x.shape
-    dev = x.device
-    st = _launch_stream(dev, stream)
+    dev = _launch_device(x)
     out = out or {}
-    _want(x, "x", (R, K), _F32_BF16, dev, dense=False)
+    xt = _float_type(x, "x")
+    _want(x, "x", (R, K), xt, dev, dense=False)
 
     def buf(name, shape, dtype):
         t = out.get(name)
         if t is None:
-            return torch.empty(shape, dtype=dtype, device=dev)
-        _want(t, name, shape, (dtype,), dev)
+            return torch.empty(shape, dtype=dtype, device=x.device)
+        _want(t, name, shape, dtype, dev)
         return t
 
     codes = buf("codes", (R, K // 2), torch.uint8)
     scales = buf("scales", (R, K // 32), torch.uint8)
     d = buf("deq", (R, K), torch.bfloat16) if deq else None
-    _check(_lib.moe_quantize_mxfp4(_ptr(x), x.dtype == torch.float32, _row_stride(x), R, K, _ptr(codes), _ptr(scales),
-                                   _ptr(d), st), "moe_quantize_mxfp4")
+    _check(_lib.moe_quantize_mxfp4(x.data_ptr(), xt is torch.float32, _row_stride(x), R, K, codes.data_ptr(),
+                                   scales.data_ptr(), _ptr(d), _launch_stream(dev, stream)), "moe_quantize_mxfp4")
     return codes, scales, d
 
 

@@ -221,21 +221,17 @@ moe_status_t moe_route_topk_grouped(const float* logits, const float* bias, int 
                                             topk_ids, topk_w, S(stream), false));
 }
 
-moe_status_t moe_route_scored(const void* logits, int in_is_bf16, int64_t row_stride, const float* bias, int T, int E,
-                              int topk, int scoring, int n_group, int topk_group, int group_score, int renormalize,
-                              float routed_scaling_factor, int32_t* topk_ids, float* topk_w, moe_stream_t stream) {
-    if (T < 0 || E < 1 || topk < 1 || n_group < 1 || topk_group < 1 || topk_group > n_group) return MOE_ERR_INVALID_ARG;
-    if (E % n_group || topk > (long long)topk_group * (E / n_group) || row_stride < E) return MOE_ERR_INVALID_ARG;
-    if (scoring != MOE_SCORE_SOFTMAX && scoring != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
-    if (group_score != MOE_GROUP_MAX && group_score != MOE_GROUP_TOP2) return MOE_ERR_INVALID_ARG;
-    if (!std::isfinite(routed_scaling_factor) || !(routed_scaling_factor > 0.0f)) return MOE_ERR_INVALID_ARG;
-    if (E > kMaxExperts || n_group > 32 || topk > kMaxTopk) return MOE_ERR_UNSUPPORTED;
-    if (T == 0) return MOE_OK;
-    if (!logits || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
-    const RouteScored r{logits, in_is_bf16 != 0, row_stride, bias,        T,
-                        E,      topk,            scoring,    n_group,     topk_group,
-                        group_score, renormalize != 0, routed_scaling_factor, topk_ids, topk_w};
-    return cuda_status(launch_route_scored(r, S(stream), false));
+moe_status_t moe_route_scored(const moe_route_args_t* p, moe_stream_t stream) {
+    if (!p || p->T < 0 || p->E < 1 || p->topk < 1) return MOE_ERR_INVALID_ARG;
+    if (p->n_group < 1 || p->topk_group < 1 || p->topk_group > p->n_group || p->E % p->n_group) return MOE_ERR_INVALID_ARG;
+    if (p->topk > (long long)p->topk_group * (p->E / p->n_group) || p->row_stride < p->E) return MOE_ERR_INVALID_ARG;
+    if (p->scoring != MOE_SCORE_SOFTMAX && p->scoring != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+    if (p->group_score != MOE_GROUP_MAX && p->group_score != MOE_GROUP_TOP2) return MOE_ERR_INVALID_ARG;
+    if (!std::isfinite(p->routed_scaling_factor) || !(p->routed_scaling_factor > 0.0f)) return MOE_ERR_INVALID_ARG;
+    if (p->E > kMaxExperts || p->n_group > 32 || p->topk > kMaxTopk) return MOE_ERR_UNSUPPORTED;
+    if (p->T == 0) return MOE_OK;
+    if (!p->logits || !p->topk_ids || !p->topk_w) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_route_scored(*p, S(stream), false));
 }
 
 moe_status_t moe_add_rmsnorm(const moe_rmsnorm_args_t* p, moe_stream_t stream) {

@@ -38,19 +38,8 @@ constexpr int kMaxTopk = 32;
 cudaError_t launch_route_topk(const float* logits, int T, int E, int topk, int32_t* ids, float* w,
                               cudaStream_t st, bool pdl);
 
-// The general routing; arguments as in moe_route_scored, validated, T >= 1.
-struct RouteScored {
-    const void* logits;
-    bool bf16;
-    long long stride;
-    const float* bias;
-    int T, E, topk, scoring, n_group, topk_group, group_score;
-    bool renorm;
-    float scale;
-    int32_t* ids;
-    float* w;
-};
-cudaError_t launch_route_scored(const RouteScored& r, cudaStream_t st, bool pdl);
+// The general routing (validated arguments, T >= 1).
+cudaError_t launch_route_scored(const moe_route_args_t& r, cudaStream_t st, bool pdl);
 
 struct PermuteWs {
     int nblk;

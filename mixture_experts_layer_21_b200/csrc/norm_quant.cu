@@ -153,13 +153,17 @@ __global__ void __launch_bounds__(256) quant_mxfp4_kernel(const void* in, long l
     pdl_launch();
 }
 
-// One block per row; thread t holds chunks t, t + blockDim, ... of eight values in registers, so
-// the row is read once.
-template <int CPT, bool F32, int Q>
-__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const moe_rmsnorm_args_t a) {
+// A block to a row (SHORT: a warp, blockDim.y of them to a block); thread t holds chunks t, t + blockDim.x of
+// eight values in registers, so the row is read once. What bounds long inputs is the memory traffic in
+// flight between the rows' barriers: the registers are held to 32 a thread, 2048 threads an SM (8192
+// rows of 7168 with residual into bf16 and MXFP8: 90 us, 5.9 TB/s; with 34 registers, a block less, 97;
+// with rows copied ahead into shared memory by blocks that walk over them 108).
+template <int CPT, bool F32, int Q, bool SHORT>
+__global__ void __launch_bounds__(1024, CPT <= 2 ? 2 : 1) add_rmsnorm_kernel(const moe_rmsnorm_args_t a) {
     __shared__ float part[32];
     pdl_wait();
-    const size_t row = blockIdx.x;
+    const size_t row = SHORT ? (size_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
+    if (SHORT && row >= a.T) return;
     const int chunks = a.H / 8;
     const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(a.residual);
     __nv_bfloat16* res_out = static_cast<__nv_bfloat16*>(a.residual_out);
@@ -185,10 +189,12 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const moe_rmsnorm_arg
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane_id() == 0) part[warp_id()] = sum;
-    __syncthreads();
-    sum = 0.0f;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) sum += part[w];
+    if (!SHORT) {
+        if (lane_id() == 0) part[warp_id()] = sum;
+        __syncthreads();
+        sum = 0.0f;
+        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) sum += part[w];
+    }
     const float rstd = 1.0f / sqrtf(sum / (float)a.H + a.eps);
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
@@ -209,12 +215,26 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const moe_rmsnorm_arg
     pdl_launch();
 }
 
-template <int CPT, bool F32>
-cudaError_t run_rmsnorm(const moe_rmsnorm_args_t& a, int threads, cudaStream_t st, bool pdl) {
-    const dim3 grid(a.T), block(threads);
-    if (a.quant == MOE_Q_MXFP8) return launch_k(add_rmsnorm_kernel<CPT, F32, MOE_Q_MXFP8>, grid, block, 0, st, pdl, a);
-    if (a.quant == MOE_Q_MXFP4) return launch_k(add_rmsnorm_kernel<CPT, F32, MOE_Q_MXFP4>, grid, block, 0, st, pdl, a);
-    return launch_k(add_rmsnorm_kernel<CPT, F32, MOE_Q_NONE>, grid, block, 0, st, pdl, a);
+template <int CPT, bool F32, bool SHORT = false>
+cudaError_t run_rmsnorm(const moe_rmsnorm_args_t& a, dim3 grid, dim3 block, cudaStream_t st, bool pdl) {
+    if (a.quant == MOE_Q_MXFP8) return launch_k(add_rmsnorm_kernel<CPT, F32, MOE_Q_MXFP8, SHORT>, grid, block, 0, st, pdl, a);
+    if (a.quant == MOE_Q_MXFP4) return launch_k(add_rmsnorm_kernel<CPT, F32, MOE_Q_MXFP4, SHORT>, grid, block, 0, st, pdl, a);
+    return launch_k(add_rmsnorm_kernel<CPT, F32, MOE_Q_NONE, SHORT>, grid, block, 0, st, pdl, a);
+}
+
+template <bool F32>
+cudaError_t run_rmsnorm(const moe_rmsnorm_args_t& a, cudaStream_t st, bool pdl) {
+    // Few rows: a row is spread as thin as it goes, for the shortest way through it. Many: two chunks
+    // a thread; rows of up to 512 values go to a warp each, eight to a block (32768 rows of 256: 19 us,
+    // a block to a row 39).
+    const int chunks = a.H / 8;
+    const bool many = a.T >= 2 * num_sms();
+    if (many && chunks <= 64) return run_rmsnorm<2, F32, true>(a, dim3((a.T + 7) / 8), dim3(32, 8), st, pdl);
+    const int cpt = chunks > 2048 ? 4 : many || chunks > 1024 ? 2 : 1;
+    const dim3 grid(a.T), block(((chunks + cpt - 1) / cpt + 31) / 32 * 32);
+    if (cpt == 1) return run_rmsnorm<1, F32>(a, grid, block, st, pdl);
+    if (cpt == 2) return run_rmsnorm<2, F32>(a, grid, block, st, pdl);
+    return run_rmsnorm<4, F32>(a, grid, block, st, pdl);
 }
 
 }  // namespace
@@ -236,21 +256,7 @@ cudaError_t launch_quant_mxfp4(const void* in, bool in_f32, long long stride, in
 }
 
 cudaError_t launch_add_rmsnorm(const moe_rmsnorm_args_t& a, cudaStream_t st, bool pdl) {
-    // Few rows: a row is spread as thin as it goes, for the shortest way through it. Many: four chunks a
-    // thread, so that more rows are in flight on an SM between their barriers.
-    const int chunks = a.H / 8;
-    const bool many = a.T >= 2 * num_sms();
-    const char* ce = getenv("CPT");
-    const int cpt = ce ? atoi(ce) : chunks > 2048 || (many && chunks >= 256) ? 4 : chunks > 1024 || (many && chunks >= 128) ? 2 : 1;
-    const int threads = ((chunks + cpt - 1) / cpt + 31) / 32 * 32;
-    if (a.x_is_f32) {
-        if (cpt == 1) return run_rmsnorm<1, true>(a, threads, st, pdl);
-        if (cpt == 2) return run_rmsnorm<2, true>(a, threads, st, pdl);
-        return run_rmsnorm<4, true>(a, threads, st, pdl);
-    }
-    if (cpt == 1) return run_rmsnorm<1, false>(a, threads, st, pdl);
-    if (cpt == 2) return run_rmsnorm<2, false>(a, threads, st, pdl);
-    return run_rmsnorm<4, false>(a, threads, st, pdl);
+    return a.x_is_f32 ? run_rmsnorm<true>(a, st, pdl) : run_rmsnorm<false>(a, st, pdl);
 }
 
 }  // namespace moe

@@ -31,13 +31,13 @@ MOE_DEV float load_logit(const void* row, int e) {
 // the other tokens occupancy.
 template <bool BF16>
 struct Token64 {
-    const RouteScored& a;
+    const moe_route_args_t& a;
     const void* row;
     float mx;     // softmax: the largest logit
     double norm;  // softmax: the sum of the scores' numerators
 
-    MOE_DEV Token64(const RouteScored& r, int t, float largest)
-        : a(r), row(static_cast<const char*>(r.logits) + (size_t)t * r.stride * (BF16 ? 2 : 4)), mx(largest), norm(1.0) {}
+    MOE_DEV Token64(const moe_route_args_t& r, int t, float largest)
+        : a(r), row(static_cast<const char*>(r.logits) + (size_t)t * r.row_stride * (BF16 ? 2 : 4)), mx(largest), norm(1.0) {}
     MOE_DEV float logit(int e) const {
         const float x = load_logit<BF16>(row, e);
         return isnan(x) ? -INFINITY : x;
@@ -79,7 +79,7 @@ __device__ __forceinline__ void values64(Token64<BF16>& k, double* c) {
 // The kept groups of a token whose c are in c[E], as bits.
 template <bool BF16>
 __device__ __forceinline__ uint32_t keep64(const Token64<BF16>& k, const double* c) {
-    const RouteScored& a = k.a;
+    const moe_route_args_t& a = k.a;
     const double ninf = -(double)INFINITY;
     // each group's largest c or the sum of its two largest (ranked by its best expert without a
     // bias, its largest logit): a power of two of lanes to a group, then lane g has group g's
@@ -112,7 +112,7 @@ __device__ __forceinline__ uint32_t keep64(const Token64<BF16>& k, const double*
 
 // The kept groups alone.
 template <bool BF16>
-__device__ __noinline__ uint32_t groups64(const RouteScored& a, int t, float mx, double* c) {
+__device__ __noinline__ uint32_t groups64(const moe_route_args_t& a, int t, float mx, double* c) {
     Token64<BF16> k(a, t, mx);
     values64(k, c);
     return keep64(k, c);
@@ -120,7 +120,7 @@ __device__ __noinline__ uint32_t groups64(const RouteScored& a, int t, float mx,
 
 // The topk best of `count` <= 32 candidates, lane i's being expert id: lane j gets the j-th.
 template <bool BF16>
-__device__ __noinline__ int order64(const RouteScored& a, int t, float mx, int id, int count) {
+__device__ __noinline__ int order64(const moe_route_args_t& a, int t, float mx, int id, int count) {
     const int lane = lane_id();
     Token64<BF16> k(a, t, mx);
     if (a.scoring == MOE_SCORE_SOFTMAX) {
@@ -149,7 +149,7 @@ __device__ __noinline__ int order64(const RouteScored& a, int t, float mx, int i
 
 // A whole token.
 template <bool BF16>
-__device__ __noinline__ void route64(const RouteScored& a, int t, double* c) {
+__device__ __noinline__ void route64(const moe_route_args_t& a, int t, double* c) {
     const int lane = lane_id(), E = a.E, gs = E / a.n_group;
     Token64<BF16> k(a, t, -INFINITY);
     if (a.scoring == MOE_SCORE_SOFTMAX) {
@@ -195,15 +195,15 @@ __device__ __noinline__ void route64(const RouteScored& a, int t, double* c) {
         __syncwarp();
     }
     double w = lane < a.topk ? k.part(k.logit(my_id)) / k.norm : 0.0;
-    if (a.renorm) {
+    if (a.renormalize) {
         double tot = w;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, off);
         w = tot > 0.0 ? w / tot : 0.0;
     }
     if (lane < a.topk) {
-        a.ids[(size_t)t * a.topk + lane] = my_id;
-        a.w[(size_t)t * a.topk + lane] = (float)((double)a.scale * w);
+        a.topk_ids[(size_t)t * a.topk + lane] = my_id;
+        a.topk_w[(size_t)t * a.topk + lane] = (float)((double)a.routed_scaling_factor * w);
     }
 }
 
@@ -238,7 +238,7 @@ MOE_DEV uint32_t key_max(const uint32_t (&k)[N]) {
 // bias rounds once more, 2^-24 |c|. Two values compare as their exact ones do if they differ by more
 // than twice the sum of both bounds (the factor of two is to spare): the slacks below. Logits compare exactly.
 template <int EPL, bool BF16, bool GROUPS>
-__device__ bool route_fast(const RouteScored& a, const float (&l)[EPL], int t, const void* row, double* c64) {
+__device__ bool route_fast(const moe_route_args_t& a, const float (&l)[EPL], int t, const void* row, double* c64) {
     const int lane = lane_id(), E = a.E;
     const bool softmax = a.scoring == MOE_SCORE_SOFTMAX;
     float mx = 0.0f, inv = 1.0f, s[EPL];
@@ -251,7 +251,7 @@ __device__ bool route_fast(const RouteScored& a, const float (&l)[EPL], int t, c
     }
     // scores of every expert, where the selection, the groups or the raw softmax weights need them
     const bool top2 = GROUPS && a.group_score == MOE_GROUP_TOP2;
-    if (a.bias || (softmax && !a.renorm) || top2) {
+    if (a.bias || (softmax && !a.renormalize) || top2) {
         if (softmax) {
             float sum = 0.0f;
 #pragma unroll
@@ -396,11 +396,11 @@ __device__ bool route_fast(const RouteScored& a, const float (&l)[EPL], int t, c
         const float x = load_logit<BF16>(row, my_id);
         const bool off = isnan(x) || x == -INFINITY;
         arg = off ? 0.0f : softmax ? x - mx : x;
-        w = off ? 0.0f : softmax ? expf(arg) * (a.renorm ? 1.0f : inv) : 1.0f / (1.0f + expf(-arg));
+        w = off ? 0.0f : softmax ? expf(arg) * (a.renormalize ? 1.0f : inv) : 1.0f / (1.0f + expf(-arg));
     }
     // far from the largest (or from 0) fp32's exponential leaves its normal range
     if (__any_sync(0xffffffffu, arg < -80.0f)) return false;
-    if (a.renorm) {
+    if (a.renormalize) {
         float tot = w;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, off);
@@ -408,8 +408,8 @@ __device__ bool route_fast(const RouteScored& a, const float (&l)[EPL], int t, c
         w /= tot;
     }
     if (mine) {
-        a.ids[(size_t)t * a.topk + lane] = my_id;
-        a.w[(size_t)t * a.topk + lane] = a.scale * w;
+        a.topk_ids[(size_t)t * a.topk + lane] = my_id;
+        a.topk_w[(size_t)t * a.topk + lane] = a.routed_scaling_factor * w;
     }
     return true;
 }
@@ -417,7 +417,7 @@ __device__ bool route_fast(const RouteScored& a, const float (&l)[EPL], int t, c
 // This lane's EPL consecutive logits, by wide loads where the rows allow them (whole 16-byte pieces
 // inside the row), NaN as -inf.
 template <int EPL, bool BF16>
-MOE_DEV void load_logits(const RouteScored& a, const void* row, bool wide, float (&l)[EPL]) {
+MOE_DEV void load_logits(const moe_route_args_t& a, const void* row, bool wide, float (&l)[EPL]) {
     constexpr int V = BF16 ? 8 : 4;  // values in 16 bytes
     const int e0 = lane_id() * EPL;
     if (EPL % V == 0 && wide) {
@@ -447,12 +447,12 @@ MOE_DEV void load_logits(const RouteScored& a, const void* row, bool wide, float
 }
 
 template <int EPL, bool BF16, bool GROUPS>
-__global__ void __launch_bounds__(128) route_scored_kernel(const RouteScored a, bool wide) {
+__global__ void __launch_bounds__(128) route_scored_kernel(const moe_route_args_t a, bool wide) {
     extern __shared__ double warps_c64[];  // [warps][E], for tokens taken up in fp64
     pdl_wait();
     const int t = blockIdx.x * (blockDim.x >> 5) + warp_id();
     if (t < a.T) {
-        const void* row = static_cast<const char*>(a.logits) + (size_t)t * a.stride * (BF16 ? 2 : 4);
+        const void* row = static_cast<const char*>(a.logits) + (size_t)t * a.row_stride * (BF16 ? 2 : 4);
         float l[EPL];
         load_logits<EPL, BF16>(a, row, wide, l);
         double* c64 = warps_c64 + warp_id() * a.E;
@@ -462,23 +462,23 @@ __global__ void __launch_bounds__(128) route_scored_kernel(const RouteScored a, 
 }
 
 template <int EPL, bool BF16>
-cudaError_t run_route(const RouteScored& r, cudaStream_t st, bool pdl) {
+cudaError_t run_route(const moe_route_args_t& r, cudaStream_t st, bool pdl) {
     const dim3 grid((r.T + 3) / 4), block(128);
     const int bytes = BF16 ? 2 : 4;
     const size_t smem = 4 * sizeof(double) * r.E;  // at most 32 KB
-    const bool wide = (reinterpret_cast<uintptr_t>(r.logits) & 15) == 0 && r.stride * bytes % 16 == 0 && r.E * bytes % 16 == 0;
+    const bool wide = (reinterpret_cast<uintptr_t>(r.logits) & 15) == 0 && r.row_stride * bytes % 16 == 0 && r.E * bytes % 16 == 0;
     if (r.topk_group < r.n_group) return launch_k(route_scored_kernel<EPL, BF16, true>, grid, block, smem, st, pdl, r, wide);
     return launch_k(route_scored_kernel<EPL, BF16, false>, grid, block, smem, st, pdl, r, wide);
 }
 
 template <int EPL>
-cudaError_t run_route(const RouteScored& r, cudaStream_t st, bool pdl) {
-    return r.bf16 ? run_route<EPL, true>(r, st, pdl) : run_route<EPL, false>(r, st, pdl);
+cudaError_t run_route(const moe_route_args_t& r, cudaStream_t st, bool pdl) {
+    return r.in_is_bf16 ? run_route<EPL, true>(r, st, pdl) : run_route<EPL, false>(r, st, pdl);
 }
 
 }  // namespace
 
-cudaError_t launch_route_scored(const RouteScored& r, cudaStream_t st, bool pdl) {
+cudaError_t launch_route_scored(const moe_route_args_t& r, cudaStream_t st, bool pdl) {
     const int epl = (r.E + 31) / 32;
     if (epl <= 1) return run_route<1>(r, st, pdl);
     if (epl <= 2) return run_route<2>(r, st, pdl);

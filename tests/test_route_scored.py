@@ -7,6 +7,8 @@ Weight tolerance, relative: scores of 32 bits carry the rounding of the exponent
 (37 * 2^-24) and three more roundings: (D + 44) 2^-24 with D the largest |l - max| or |l| of a row's
 chosen experts; twice that where the chosen scores are summed and divided again.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -19,30 +21,40 @@ INVALID, UNSUP = 1, 2
 
 
 def _call(**kw):
-    d = dict(logits=16, bf16=0, stride=None, bias=None, T=4, E=16, topk=2, scoring=0, ng=1, tg=1, gs=0, renorm=1,
-             scale=1.0, ids=16, w=16)
+    d = dict(logits=16, in_is_bf16=0, row_stride=None, bias=None, T=4, E=16, topk=2, scoring=0, n_group=1, topk_group=1,
+             group_score=0, renormalize=1, routed_scaling_factor=1.0, topk_ids=16, topk_w=16)
     d.update(kw)
-    return L.moe_route_scored(d["logits"], d["bf16"], d["E"] if d["stride"] is None else d["stride"], d["bias"], d["T"],
-                              d["E"], d["topk"], d["scoring"], d["ng"], d["tg"], d["gs"], d["renorm"], d["scale"],
-                              d["ids"], d["w"], None)
+    if d["row_stride"] is None:
+        d["row_stride"] = d["E"]
+    return L.moe_route_scored(ctypes.byref(m.moe_route_args_t(**d)), None)
 
 
-@pytest.mark.parametrize("kw", [dict(T=-1), dict(E=0), dict(topk=0), dict(topk=17), dict(stride=15), dict(stride=0),
-                                dict(stride=-16), dict(scoring=2), dict(scoring=-1), dict(ng=0), dict(ng=3),
-                                dict(ng=4, tg=0), dict(ng=4, tg=5), dict(ng=8, tg=1, topk=3), dict(gs=2),
-                                dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf")),
-                                dict(logits=None), dict(ids=None), dict(w=None)])
+@pytest.mark.parametrize("kw", [dict(T=-1), dict(E=0), dict(topk=0), dict(topk=17), dict(row_stride=15),
+                                dict(row_stride=0), dict(row_stride=-16), dict(scoring=2), dict(scoring=-1),
+                                dict(n_group=0), dict(n_group=3), dict(n_group=4, topk_group=0),
+                                dict(n_group=4, topk_group=5), dict(n_group=8, topk_group=1, topk=3),
+                                dict(group_score=2), dict(routed_scaling_factor=0.0),
+                                dict(routed_scaling_factor=float("nan")), dict(routed_scaling_factor=float("inf")),
+                                dict(logits=None), dict(topk_ids=None), dict(topk_w=None)])
 def test_refuses_bad_arguments(kw):
     assert _call(**kw) == INVALID
 
 
-@pytest.mark.parametrize("kw", [dict(E=1025), dict(E=66, ng=33, tg=33), dict(E=64, topk=33)])
+@pytest.mark.parametrize("kw", [dict(E=1025), dict(E=66, n_group=33, topk_group=33), dict(E=64, topk=33)])
 def test_refuses_unsupported_sizes(kw):
     assert _call(**kw) == UNSUP
 
 
+def test_packed_arguments_have_the_structures_layout():
+    for pack, cls in ((m._ROUTE_ARGS, m.moe_route_args_t), (m._RMSNORM_ARGS, m.moe_rmsnorm_args_t)):
+        vals = [1000 + i for i in range(len(cls._fields_))]
+        a = cls.from_buffer_copy(pack.pack(*vals).ljust(ctypes.sizeof(cls), b"\0"))
+        assert [getattr(a, f[0]) for f in cls._fields_] == vals
+
+
 def test_no_tokens_is_a_no_op():
-    assert _call(T=0, logits=None, ids=None, w=None) == 0
+    assert _call(T=0, logits=None, topk_ids=None, topk_w=None) == 0
+    assert L.moe_route_scored(None, None) == INVALID
 
 
 @pytest.mark.parametrize("bad", ["dtype", "cpu", "bias", "cols"])
