@@ -182,29 +182,31 @@ def _launch_stream(dev: int, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _want(t, name: str, shape, dtype, dev: int, dense: bool = True) -> None:
+def _want(t, name: str, shape, dtype, dev: int, dense: bool = True) -> int:
     """A tensor argument of this shape and type on this device; rows contiguous, and dense unless the
-    call takes a row stride."""
+    call takes a row stride. Returns the elements between rows, 0 where they follow one another."""
     if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
         if t.is_contiguous():
-            return
+            return 0
         if not dense and (t.shape[1] <= 1 or t.stride(1) == 1) and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1]):
-            return
+            return t.stride(0) if t.shape[0] > 1 else 0
         raise ValueError(f"{name}: need {'a contiguous tensor' if dense else 'contiguous rows that do not overlap'}, "
                          f"got strides {t.stride()}")
     raise ValueError(f"{name}: need {tuple(shape)} {dtype} on cuda:{dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def _output(out, name: str, like, shape, dtype, dev: int, dense: bool = True):
+    """The caller's output of that name, checked, or a new one; and its row stride."""
+    t = out.get(name)
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device), 0
+    return t, _want(t, name, shape, dtype, dev, dense)
 
 
 def _float_type(t, name: str) -> torch.dtype:
     if t.dtype is torch.bfloat16 or t.dtype is torch.float32:
         return t.dtype
     raise ValueError(f"{name}: need bf16 or fp32, got {t.dtype}")
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    """Elements between rows (a single row's stride is not used)."""
-    rows, cols = t.shape
-    return cols if rows <= 1 or t.is_contiguous() else t.stride(0)
 
 
 def version() -> str:
@@ -305,7 +307,7 @@ def moe_route_scored(logits: torch.Tensor, topk: int, scoring: str = "softmax", 
     T, E = logits.shape
     dev = _launch_device(logits)
     dt = _float_type(logits, "logits")
-    _want(logits, "logits", (T, E), dt, dev, dense=False)
+    stride = _want(logits, "logits", (T, E), dt, dev, False) or E
     if bias is not None:
         _want(bias, "bias", (E,), torch.float32, dev)
     if ids is None:
@@ -317,7 +319,7 @@ def moe_route_scored(logits: torch.Tensor, topk: int, scoring: str = "softmax", 
     else:
         _want(w, "w", (T, topk), torch.float32, dev)
     a = _ROUTE_ARGS.pack(logits.data_ptr(), 0 if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr(),
-                         _row_stride(logits), dt is torch.bfloat16, T, E, topk, SCORING[scoring], n_group, topk_group,
+                         stride, dt is torch.bfloat16, T, E, topk, SCORING[scoring], n_group, topk_group,
                          GROUP_SCORE[group_score], renormalize, routed_scaling_factor)
     _check(_lib.moe_route_scored(a, _launch_stream(dev, stream)), "moe_route_scored")
     return ids, w
@@ -336,36 +338,33 @@ def moe_add_rmsnorm(x: torch.Tensor, weight=None, residual=None, eps: float = 1e
     T, H = x.shape
     dev = _launch_device(x)
     out = out or {}
-    bf16, u8, shape = torch.bfloat16, torch.uint8, (T, H)
+    bf16, shape = torch.bfloat16, (T, H)
     xt = _float_type(x, "x")
-    _want(x, "x", shape, xt, dev, dense=False)
+    sx = _want(x, "x", shape, xt, dev, False)
+    y = r = codes = scales = d = None
+    sres = sr = sy = pres = pw = pr = py = pc = ps = pd = w32 = 0
     if residual is not None:
-        _want(residual, "residual", shape, bf16, dev, dense=False)
+        sres, pres = _want(residual, "residual", shape, bf16, dev, False), residual.data_ptr()
+        r, sr = _output(out, "residual", x, shape, bf16, dev, False)
+        pr = r.data_ptr()
     if weight is not None:
-        _want(weight, "weight", (H,), _float_type(weight, "weight"), dev)
-    if deq and quant is None:
-        raise ValueError("deq needs quant")
-
-    def buf(name, shape, dtype, dense):
-        t = out.get(name)
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=x.device)
-        _want(t, name, shape, dtype, dev, dense)
-        return t
-
-    r = None if residual is None else buf("residual", shape, bf16, False)
-    y = buf("y", shape, bf16, False) if want_y else None
-    codes = scales = d = None
-    if quant is not None:
-        codes = buf("codes", (T, H // 2) if quant == "mxfp4" else shape, u8, True)
-        scales = buf("scales", (T, H // 32), u8, True)
+        wt = _float_type(weight, "weight")
+        _want(weight, "weight", (H,), wt, dev)
+        pw, w32 = weight.data_ptr(), wt is not bf16
+    if want_y:
+        y, sy = _output(out, "y", x, shape, bf16, dev, False)
+        py = y.data_ptr()
+    q = QUANT[quant]
+    if q:
+        codes, _ = _output(out, "codes", x, (T, H // 2) if q == 2 else shape, torch.uint8, dev)
+        scales, _ = _output(out, "scales", x, (T, H // 32), torch.uint8, dev)
+        pc, ps = codes.data_ptr(), scales.data_ptr()
         if deq:
-            d = buf("deq", shape, bf16, True)
-    p = lambda t: 0 if t is None else t.data_ptr()
-    a = _RMSNORM_ARGS.pack(x.data_ptr(), p(residual), p(weight), xt is not bf16,
-                           weight is not None and weight.dtype is not bf16, T, H, _row_stride(x),
-                           0 if residual is None else _row_stride(residual), 0 if r is None else _row_stride(r),
-                           0 if y is None else _row_stride(y), eps, QUANT[quant], p(r), p(y), p(codes), p(scales), p(d))
+            d, _ = _output(out, "deq", x, shape, bf16, dev)
+            pd = d.data_ptr()
+    elif deq:
+        raise ValueError("deq needs quant")
+    a = _RMSNORM_ARGS.pack(x.data_ptr(), pres, pw, xt is not bf16, w32, T, H, sx, sres, sr, sy, eps, q, pr, py, pc, ps, pd)
     _check(_lib.moe_add_rmsnorm(a, _launch_stream(dev, stream)), "moe_add_rmsnorm")
     return dict(residual=r, y=y, codes=codes, scales=scales, deq=d)
 
@@ -537,20 +536,12 @@ def moe_quantize_mxfp4(x: torch.Tensor, deq: bool = False, out=None, stream=None
     dev = _launch_device(x)
     out = out or {}
     xt = _float_type(x, "x")
-    _want(x, "x", (R, K), xt, dev, dense=False)
-
-    def buf(name, shape, dtype):
-        t = out.get(name)
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=x.device)
-        _want(t, name, shape, dtype, dev)
-        return t
-
-    codes = buf("codes", (R, K // 2), torch.uint8)
-    scales = buf("scales", (R, K // 32), torch.uint8)
-    d = buf("deq", (R, K), torch.bfloat16) if deq else None
-    _check(_lib.moe_quantize_mxfp4(x.data_ptr(), xt is torch.float32, _row_stride(x), R, K, codes.data_ptr(),
-                                   scales.data_ptr(), _ptr(d), _launch_stream(dev, stream)), "moe_quantize_mxfp4")
+    stride = _want(x, "x", (R, K), xt, dev, False) or K
+    codes, _ = _output(out, "codes", x, (R, K // 2), torch.uint8, dev)
+    scales, _ = _output(out, "scales", x, (R, K // 32), torch.uint8, dev)
+    d = _output(out, "deq", x, (R, K), torch.bfloat16, dev)[0] if deq else None
+    _check(_lib.moe_quantize_mxfp4(x.data_ptr(), xt is torch.float32, stride, R, K, codes.data_ptr(), scales.data_ptr(),
+                                   _ptr(d), _launch_stream(dev, stream)), "moe_quantize_mxfp4")
     return codes, scales, d
 
 
