@@ -211,34 +211,65 @@ __device__ __noinline__ void route64(const moe_route_args_t& a, int t, double* c
 // The order of floats as unsigned integers; 0 is below -inf.
 MOE_DEV uint32_t order_key(float f) {
     const uint32_t u = __float_as_uint(f + 0.0f);  // -0 as +0
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 MOE_DEV float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
-// The largest key of an array, by a tree.
+// Keys in descending order, by Batcher's odd-even merge sort (K. E. Batcher, Sorting networks and their
+// applications, 1968); N a power of two.
 template <int N>
-MOE_DEV uint32_t key_max(const uint32_t (&k)[N]) {
-    uint32_t m[N];
+MOE_DEV void sort_keys(uint32_t (&k)[N]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) m[i] = k[i];
+    for (int p = 1; p < N; p *= 2)
 #pragma unroll
-    for (int w = N / 2; w > 0; w >>= 1)
+        for (int q = p; q >= 1; q /= 2)
 #pragma unroll
-        for (int i = 0; i < w; ++i) m[i] = max(m[i], m[i + w]);
-    return m[0];
+            for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const uint32_t hi = max(k[i + j], k[i + j + q]);
+                        k[i + j + q] = min(k[i + j], k[i + j + q]);
+                        k[i + j] = hi;
+                    }
 }
 
+MOE_DEV float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+MOE_DEV float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// What the host works out once for the launch.
+struct RoutePlan {
+    bool wide;        // the rows' 16-byte pieces lie inside them and aligned
+    bool wide_bias;   // and those of the bias, with E = 32 EPL
+    int gs;           // experts to a group
+    int lanes, shift; // GROUPS: a group is an aligned run of `lanes` = 2^shift lanes; lanes = 0: it is not
+};
+
 // One token, in fp32 where that decides. False where it cannot (infinite logits, more than 32
-// candidates within the error of each other); nothing is written then.
+// candidates within the error of each other); nothing is written then. What bounds it is the number
+// of instructions (about 700 a token with 256 experts in 8 groups, at 1600 36 us for 16384 tokens).
 //
-// Error of the scores. expf is within 2 units in the last place. Sigmoid: the sum 1 + e rounds once
-// and __fdividef is within 2 units, so s <= 1 is within 4 * 2^-23 = 2^-21. Softmax: the argument l - max rounds,
-// which moves e^(l - max) by at most 2^-25, and the sum of up to 1024 terms, a chain of 32 in a lane
-// and 5 across, is within 37 * 2^-24: s is within 2^-18 of itself and 2^-22 of the largest. Adding the
-// bias rounds once more, 2^-24 |c|. Two values compare as their exact ones do if they differ by more
-// than twice the sum of both bounds (the factor of two is to spare): the slacks below. Logits compare exactly.
+// Error of the scores that rank. Sigmoid: the exponential's argument -l log2(e) rounds twice, 2^-23 |l|
+// relative to the exponential e, whose approximation is within 2^-22; e / (1 + e)^2 <= 1/4 and |l| e / (1 + e)^2
+// <= 0.23 bring that to 2^-23 in s; the sum rounds once and the reciprocal is within 2^-23: s is within 2^-21.
+// Softmax: the argument (l - max) log2(e) rounds three times; |x| e^-|x| <= 0.37, so a term is within 2^-22 of
+// the largest and, weighted by the terms, whose mean |x| is at most ln 1024 < 7, the sum within 13 * 2^-23,
+// and 37 * 2^-24 for its additions, a chain of 32 in a lane and 5 across: s is within 2^-18 of itself and
+// 2^-22 of the largest. (Raw softmax weights take the exact exponential for their sum.) Adding the bias
+// rounds once more, 2^-24 |c|. Two values compare as their exact ones do if they differ by more than the
+// sum of both bounds; the slacks below are twice that. Logits compare exactly.
 template <int EPL, bool BF16, bool GROUPS>
-__device__ bool route_fast(const moe_route_args_t& a, const float (&l)[EPL], int t, const void* row, double* c64) {
+__device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, const float (&l)[EPL], int t,
+                           const void* row, double* c64) {
+    constexpr float LOG2E = 1.44269504f;
     const int lane = lane_id(), E = a.E;
     const bool softmax = a.scoring == MOE_SCORE_SOFTMAX;
     float mx = 0.0f, inv = 1.0f, s[EPL];
@@ -251,12 +282,13 @@ __device__ bool route_fast(const moe_route_args_t& a, const float (&l)[EPL], int
     }
     // scores of every expert, where the selection, the groups or the raw softmax weights need them
     const bool top2 = GROUPS && a.group_score == MOE_GROUP_TOP2;
-    if (a.bias || (softmax && !a.renormalize) || top2) {
+    const bool raw = softmax && !a.renormalize;
+    if (a.bias || raw || top2) {
         if (softmax) {
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
-                s[i] = expf(l[i] - mx);  // 0 where masked
+                s[i] = raw ? expf(l[i] - mx) : exp2_approx((l[i] - mx) * LOG2E);  // 0 where masked
                 sum += s[i];
             }
 #pragma unroll
@@ -266,7 +298,7 @@ __device__ bool route_fast(const moe_route_args_t& a, const float (&l)[EPL], int
             for (int i = 0; i < EPL; ++i) s[i] *= inv;
         } else {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) s[i] = __fdividef(1.0f, 1.0f + expf(-l[i]));
+            for (int i = 0; i < EPL; ++i) s[i] = rcp_approx(1.0f + exp2_approx(l[i] * -LOG2E));
         }
     }
     // what ranks the experts, as order keys: c, or the logits; below them masked experts (-inf),
@@ -274,53 +306,73 @@ __device__ bool route_fast(const moe_route_args_t& a, const float (&l)[EPL], int
     uint32_t key[EPL];
     float bmax = 0.0f;
     const int live = min(max(E - lane * EPL, 0), EPL);  // this lane's experts
+    if (a.bias) {
+        float b[EPL];
+        if (EPL % 4 == 0 && plan.wide_bias) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        float v = l[i];
-        if (a.bias && i < live) {
-            const float b = __ldg(a.bias + lane * EPL + i);
-            bmax = fmaxf(bmax, fabsf(b));
-            if (l[i] > -INFINITY) v = s[i] + b;
+            for (int q = 0; q < EPL / 4; ++q) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(a.bias + lane * EPL) + q);
+                b[4 * q] = f.x;
+                b[4 * q + 1 % EPL] = f.y;
+                b[4 * q + 2 % EPL] = f.z;
+                b[4 * q + 3 % EPL] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) b[i] = i < live ? __ldg(a.bias + lane * EPL + i) : 0.0f;
         }
-        key[i] = i < live ? order_key(v) : 0u;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            bmax = fmaxf(bmax, fabsf(b[i]));
+            key[i] = order_key(l[i] > -INFINITY ? s[i] + b[i] : -INFINITY);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) key[i] = order_key(l[i]);
+    }
+    if (live < EPL) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (i >= live) key[i] = 0u;
     }
     if (a.bias) bmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
     if (GROUPS) {
-        const int gs = E / a.n_group;
-        // each group's two largest values; lane g keeps group g's score
+        const int gs = plan.gs;
+        // each group's two largest keys of c (of s without a bias; of the logits where the best expert
+        // ranks the group); lane g keeps group g's score
+        auto group_key = [&](int i) {
+            return top2 && !a.bias && key[i] > order_key(-INFINITY) ? order_key(s[i]) : key[i];
+        };
+        auto merge = [](uint32_t& a1, uint32_t& a2, uint32_t b1, uint32_t b2) {
+            a2 = max(min(a1, b1), max(a2, b2));
+            a1 = max(a1, b1);
+        };
+        auto score = [&](uint32_t a1, uint32_t a2) {
+            const float best = a1 ? key_value(a1) : -INFINITY;
+            return top2 && a2 > order_key(-INFINITY) ? best + key_value(a2) : best;
+        };
+        const int lanes = plan.lanes;
         float my = -INFINITY;
-        auto merge = [](float& a1, float& a2, float b1, float b2) {
-            a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
-            a1 = fmaxf(a1, b1);
-        };
-        auto value = [&](int i) {  // c (s without a bias), or the logit where the best expert's ranks the group
-            if (top2 && !a.bias) return l[i] > -INFINITY ? s[i] : -INFINITY;
-            return key_value(key[i]);
-        };
-        auto score = [&](float a1, float a2) { return a1 + (top2 && a2 > -INFINITY ? a2 : 0.0f); };
-        const int lanes = gs / EPL;
-        const bool runs = gs % EPL == 0 && (lanes & (lanes - 1)) == 0;  // a group is an aligned run of lanes
-        if (runs) {
-            float a1 = -INFINITY, a2 = -INFINITY;
+        if (lanes) {
+            uint32_t a1 = 0u, a2 = 0u;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (i < live) merge(a1, a2, value(i), -INFINITY);
+            for (int i = 0; i < EPL; ++i) merge(a1, a2, group_key(i), 0u);
             for (int off = 1; off < lanes; off <<= 1) {
-                const float b1 = __shfl_xor_sync(0xffffffffu, a1, off), b2 = __shfl_xor_sync(0xffffffffu, a2, off);
+                const uint32_t b1 = __shfl_xor_sync(0xffffffffu, a1, off), b2 = __shfl_xor_sync(0xffffffffu, a2, off);
                 merge(a1, a2, b1, b2);
             }
             my = __shfl_sync(0xffffffffu, score(a1, a2), min(lane * lanes, 31));
         } else {
             for (int g = 0; g < a.n_group; ++g) {
-                float a1 = -INFINITY, a2 = -INFINITY;
+                uint32_t a1 = 0u, a2 = 0u;
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {
                     const int e = lane * EPL + i - g * gs;
-                    if (e >= 0 && e < gs) merge(a1, a2, value(i), -INFINITY);
+                    if (e >= 0 && e < gs) merge(a1, a2, group_key(i), 0u);
                 }
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) {
-                    const float b1 = __shfl_xor_sync(0xffffffffu, a1, off), b2 = __shfl_xor_sync(0xffffffffu, a2, off);
+                    const uint32_t b1 = __shfl_xor_sync(0xffffffffu, a1, off), b2 = __shfl_xor_sync(0xffffffffu, a2, off);
                     merge(a1, a2, b1, b2);
                 }
                 if (lane == g) my = score(a1, a2);
@@ -339,8 +391,8 @@ __device__ bool route_fast(const moe_route_args_t& a, const float (&l)[EPL], int
             const float slack = (softmax ? 0x1p-17f * 2.0f + 0x1p-19f : 0x1p-20f * 4.0f) + 0x1p-22f * 4.0f * (1.0f + bmax);
             if (!(lo - hi > slack)) keep = groups64<BF16>(a, t, mx, c64);
         }
-        if (runs) {
-            const int g = lane / lanes;
+        if (lanes) {
+            const int g = lane >> plan.shift;
             if (g < a.n_group && !(keep >> g & 1u)) {
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) key[i] = 0u;
@@ -351,48 +403,66 @@ __device__ bool route_fast(const moe_route_args_t& a, const float (&l)[EPL], int
                 if (i < live && !(keep >> ((lane * EPL + i) / gs) & 1u)) key[i] = 0u;
         }
     }
-    // top-k: each lane's best, the warp's best, the lowest lane that has it, its lowest expert. With a
-    // bias the candidates go on to those within the error of the last chosen, and where two
+    // Top-k: every lane sorts its keys, and the warp takes the largest of the lanes' heads, the lowest
+    // lane's among equal ones. Which of the lane's experts a key is, is looked up afterwards from the
+    // unsorted keys in shared memory; of a lane's equal keys the n-th taken is the n-th in order of id.
+    // With a bias the candidates go on to those within the error of the last chosen, and where two
     // neighbours are that close, fp64 orders the candidates: any other expert is below topk of them.
-    float prev = 0.0f, last = 0.0f;
-    int my_id = 0, count = 0;
+    uint32_t* keys = reinterpret_cast<uint32_t*>(c64);  // [32][EPL]
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) keys[lane * EPL + i] = key[i];
+    sort_keys<EPL>(key);
+    uint32_t taken = 0u, my_key = 0u;  // the lane's last key taken; the key of candidate `lane`
+    int equals = 0, my_equals = 0, my_from = 0, count = 0;
+    // the slack of two c: s_i + s_j <= |c_i| + |c_j| + 2 bmax for softmax; sigmoid's s are at most 1
+    const float slack0 = softmax ? 0x1p-16f * bmax + 0x1p-20f * inv : 0x1p-19f + 0x1p-21f * (1.0f + bmax);
+    const float slack1 = softmax ? 0x1p-17f + 0x1p-22f : 0.0f;
+    float prev = INFINITY, last = INFINITY;
     bool close = false;
     for (int j = 0;; ++j) {
         if (j >= a.topk && !a.bias) break;
-        const uint32_t best = key_max<EPL>(key);
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, key[0]);
         if (top == 0u) break;  // none left; the kept groups hold at least topk experts
         if (a.bias) {
             const float c = key_value(top);
-            auto near = [&](float hi) {  // masked experts (-inf) are behind every live one, in order of id
-                if (!(c > -INFINITY)) return false;
-                const float ac = fabsf(hi) + fabsf(c);
-                const float sb = fminf(2.0f, ac + 2.0f * bmax);  // s_i + s_j <= |c_i| + |c_j| + |b_i| + |b_j|
-                return !(hi - c > (softmax ? 0x1p-17f * sb + 0x1p-20f * inv : 0x1p-19f) + 0x1p-22f * ac);
-            };
+            // masked experts (c = -inf, no slack) are behind every live one, in order of id
+            auto near = [&](float hi) { return c > -INFINITY && !(hi - c > slack0 + slack1 * (fabsf(hi) + fabsf(c))); };
             if (j >= a.topk && !near(last)) break;
             if (j && near(prev)) close = true;
             prev = c;
             if (j < a.topk) last = c;
         }
         if (j == 32) return false;
-        const int from = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-        int bi = 0;
+        const int from = __ffs(__ballot_sync(0xffffffffu, key[0] == top)) - 1;
+        const int same = taken == top ? equals + 1 : 0;  // of the lane that is taken from
+        const int theirs = __shfl_sync(0xffffffffu, same, from);
+        if (lane == j) {
+            my_key = top;
+            my_from = from;
+            my_equals = theirs;
+        }
+        if (lane == from) {
+            taken = top;
+            equals = same;
 #pragma unroll
-        for (int i = EPL - 1; i >= 0; --i)
-            if (key[i] == top) bi = i;
-        const int id = __shfl_sync(0xffffffffu, bi, from) + from * EPL;
-        if (lane == j) my_id = id;
+            for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
+            key[EPL - 1] = 0u;
+        }
         count = j + 1;
+    }
+    __syncwarp();
+    int my_id = 0;
+    if (lane < count) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (lane == from && i == bi) key[i] = 0u;
+            if (keys[my_from * EPL + i] == my_key && my_equals-- == 0) my_id = my_from * EPL + i;
     }
     if (close) my_id = order64<BF16>(a, t, mx, my_id, count);
     const bool mine = lane < a.topk;
     float w = 0.0f, arg = 0.0f;
     if (mine) {
-        // the chosen logit once more (from the cache): its score with an exact division
+        // the chosen logit once more (from the cache): its score with exact functions
         const float x = load_logit<BF16>(row, my_id);
         const bool off = isnan(x) || x == -INFINITY;
         arg = off ? 0.0f : softmax ? x - mx : x;
@@ -447,16 +517,16 @@ MOE_DEV void load_logits(const moe_route_args_t& a, const void* row, bool wide, 
 }
 
 template <int EPL, bool BF16, bool GROUPS>
-__global__ void __launch_bounds__(128) route_scored_kernel(const moe_route_args_t a, bool wide) {
-    extern __shared__ double warps_c64[];  // [warps][E], for tokens taken up in fp64
+__global__ void __launch_bounds__(128) route_scored_kernel(const moe_route_args_t a, const RoutePlan plan) {
+    extern __shared__ double warps_c64[];  // [warps]: 32 EPL keys, or E values of a token taken up in fp64
     pdl_wait();
     const int t = blockIdx.x * (blockDim.x >> 5) + warp_id();
     if (t < a.T) {
         const void* row = static_cast<const char*>(a.logits) + (size_t)t * a.row_stride * (BF16 ? 2 : 4);
         float l[EPL];
-        load_logits<EPL, BF16>(a, row, wide, l);
-        double* c64 = warps_c64 + warp_id() * a.E;
-        if (!route_fast<EPL, BF16, GROUPS>(a, l, t, row, c64)) route64<BF16>(a, t, c64);
+        load_logits<EPL, BF16>(a, row, plan.wide, l);
+        double* c64 = warps_c64 + warp_id() * (32 * EPL);
+        if (!route_fast<EPL, BF16, GROUPS>(a, plan, l, t, row, c64)) route64<BF16>(a, t, c64);
     }
     pdl_launch();
 }
@@ -465,10 +535,17 @@ template <int EPL, bool BF16>
 cudaError_t run_route(const moe_route_args_t& r, cudaStream_t st, bool pdl) {
     const dim3 grid((r.T + 3) / 4), block(128);
     const int bytes = BF16 ? 2 : 4;
-    const size_t smem = 4 * sizeof(double) * r.E;  // at most 32 KB
-    const bool wide = (reinterpret_cast<uintptr_t>(r.logits) & 15) == 0 && r.row_stride * bytes % 16 == 0 && r.E * bytes % 16 == 0;
-    if (r.topk_group < r.n_group) return launch_k(route_scored_kernel<EPL, BF16, true>, grid, block, smem, st, pdl, r, wide);
-    return launch_k(route_scored_kernel<EPL, BF16, false>, grid, block, smem, st, pdl, r, wide);
+    const size_t smem = 4 * sizeof(double) * 32 * EPL;  // at most 32 KB
+    RoutePlan p{};
+    p.wide = (reinterpret_cast<uintptr_t>(r.logits) & 15) == 0 && r.row_stride * bytes % 16 == 0 && r.E * bytes % 16 == 0;
+    p.wide_bias = (reinterpret_cast<uintptr_t>(r.bias) & 15) == 0 && r.E == 32 * EPL;
+    p.gs = r.E / r.n_group;
+    if (p.gs % EPL == 0 && ((p.gs / EPL) & (p.gs / EPL - 1)) == 0) {
+        p.lanes = p.gs / EPL;
+        while ((1 << p.shift) < p.lanes) ++p.shift;
+    }
+    if (r.topk_group < r.n_group) return launch_k(route_scored_kernel<EPL, BF16, true>, grid, block, smem, st, pdl, r, p);
+    return launch_k(route_scored_kernel<EPL, BF16, false>, grid, block, smem, st, pdl, r, p);
 }
 
 template <int EPL>
