@@ -625,22 +625,24 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
 
     // After an abort (PAIR: always; in a normal run these waits return at once) every role lets what
     // it has in flight finish, so that no memory is released, or left by a CTA of the pair, in use.
+    // Copies get about 100 microseconds a stage, far longer than one takes: after an abort the leader's
+    // barriers may wait for copies that the peer never issued.
     tc_fence_before();
     __syncthreads();
     if (PAIR || *abort_flag) {
         int never = 0;
+        constexpr long long COPY_LIMIT = 200000;
         const bool scale = warp >= C::SCALE_WARP0 && warp < C::GATHER_WARP0;
         if (scale) {  // entry d is always the same warp's: its latest copy is the one to wait for
             for (int d = 0; d < kSfRing; ++d)
-                if (is.mask >> d & 1u) mbar_wait(&mc->sf_ready[d], is.par >> d & 1u, &never);
+                if (is.mask >> d & 1u) mbar_wait(&mc->sf_ready[d], is.par >> d & 1u, &never, COPY_LIMIT);
         } else if (warp == 0 && leader) {
             for (int q = 0; q < C::STAGES; ++q)
-                if (is.mask >> q & 1u) mbar_wait(&ctl->full[q], is.par >> q & 1u, &never);
+                if (is.mask >> q & 1u) mbar_wait(&ctl->full[q], is.par >> q & 1u, &never, COPY_LIMIT);
         } else if (warp == 0 && is.mask && *abort_flag) {
-            // the peer's copies complete on the leader's barriers; those of a stage the leader never
-            // armed are not tracked: about 100 microseconds, far longer than a copy takes
+            // the peer's copies complete on the leader's barriers, which it cannot watch
             const long long t0 = clock64();
-            while (clock64() - t0 < 200000) {
+            while (clock64() - t0 < COPY_LIMIT) {
             }
         }
         if (is.tc) {

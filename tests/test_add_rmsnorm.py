@@ -185,3 +185,35 @@ def test_binding_refuses_bad_tensors():
         m.moe_add_rmsnorm(torch.zeros(64, 4, dtype=torch.bfloat16, device="cuda").t())
     with pytest.raises(m.MoEError):
         m.moe_add_rmsnorm(torch.zeros(4, 68, dtype=torch.bfloat16, device="cuda")[:, 4:], weight=None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [32, 96, 512, 544])
+@pytest.mark.parametrize("T", [296, 301, 1000])
+def test_many_short_rows(T, H):
+    """Rows of up to 512 values share a block, a warp each; the last block is not full."""
+    _run(T, H, False, True, "bf16", "mxfp4", deq=True)
+    _run(T, H, True, False, "f32", "mxfp8")
+
+
+@pytest.mark.gpu
+def test_graph_and_stream():
+    """On a side stream, and captured and replayed on new rows."""
+    x, r, w = (None if t is None else t.cuda() for t in _inputs(70, 512, False, True, "bf16", 4))
+    out = dict(y=torch.empty_like(x), residual=torch.empty_like(x),
+               codes=torch.empty(70, 256, dtype=torch.uint8, device="cuda"),
+               scales=torch.empty(70, 16, dtype=torch.uint8, device="cuda"))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    m.moe_add_rmsnorm(x, w, r, 1e-5, "mxfp4", out=out, stream=side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.moe_add_rmsnorm(x, w, r, 1e-5, "mxfp4", out=out)
+    x2 = _inputs(70, 512, False, True, "bf16", 5)[0].cuda()
+    x.copy_(x2)
+    g.replay()
+    torch.cuda.synchronize()
+    want = m.moe_add_rmsnorm(x2, w, r, 1e-5, "mxfp4")
+    for k in out:
+        assert torch.equal(out[k], want[k])

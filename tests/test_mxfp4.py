@@ -17,7 +17,7 @@ import workloads as W
 from oracle import moe_oracle as O
 
 L = m.lib()
-INVALID, UNSUP, ALIGN, WS_SMALL, NOT_PREP, DEVICE = 1, 2, 3, 4, 8, 6
+INVALID, UNSUP, ALIGN, WS_SMALL, NOT_PREP, DEVICE, TIMEOUT = 1, 2, 3, 4, 8, 6, 7
 
 
 # ------------------------------------------------------------------ refusals (CPU)
@@ -229,6 +229,60 @@ def test_product_many_tiles():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("tile", ["16", "32", "64", "128", "pairs"])
+@pytest.mark.parametrize("lens,N,K", [([1, 0, 37, 200, 16, 129, 0], 200, 544), ([385, 31, 250], 640, 1824)])
+def test_product_every_tile(lens, N, K, tile, gather, monkeypatch):
+    """Every token tile and the CTA pairs, on segments shorter and longer than the tile: an odd number
+    of weight blocks, a ring of stages that turns several times, tiles that follow one another on an SM."""
+    monkeypatch.setenv("MOE_GEMM_PAIRS", "1" if tile == "pairs" else "0")
+    if tile != "pairs":
+        monkeypatch.setenv("MOE_TOKEN_TILE", tile)
+    _check_product(_case(lens, N, K, gather, seed=len(lens), alpha=True, pad=3))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("pairs", ["0", "1"])
+def test_product_same_bits_many_times(pairs, gather, monkeypatch):
+    """Long runs of the pipeline, over and over: 16 stages a tile, many tiles an SM, the same bits each time."""
+    monkeypatch.setenv("MOE_GEMM_PAIRS", pairs)
+    case = _case([700, 513, 190, 64], 4096, 4096, gather, seed=21, T=800)
+    ac, asc, wc, wsc, idx, al, cu, M = case
+    w = m.moe_prepare_weights(m.Weight("mxfp4", wc.cuda(), wsc.cuda()))
+    args = [t.cuda() for t in (ac, asc)] + [w, cu.cuda(), None if idx is None else idx.cuda()]
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    want = m.moe_grouped_gemm_mxfp4(*args, ws=ws)
+    for _ in range(50):
+        assert torch.equal(m.moe_grouped_gemm_mxfp4(*args, ws=ws), want)
+    assert m.moe_get_device_error(ws) == 0
+    rows = [0, 699, 700, 1212, 1300, M - 1]           # and sampled rows against 64 bits
+    a = O.mxfp4_dequantize_rows(O.unpack_e2m1(ac.numpy()), asc.numpy())
+    seg = np.searchsorted(cu.numpy(), rows, side="right")
+    for r, g in zip(rows, seg):
+        v = a[r if idx is None else int(idx[r])]
+        wv = O.mxfp4_dequantize_rows(O.unpack_e2m1(wc[g].numpy()), wsc[g].numpy())
+        ref, mag = wv @ v, np.abs(wv) @ np.abs(v)
+        slack = (4096 / 64 + 1) * 2.0 ** -22 * mag
+        assert np.all(np.abs(want[r].double().cpu().numpy() - ref) <= slack + (np.abs(ref) + slack) * 2.0 ** -8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("pairs", ["0", "1"])
+def test_product_wait_limit(pairs, gather, monkeypatch):
+    """A pipeline wait that runs out is reported, the kernel returns by itself, and the next call on the
+    same workspace is right."""
+    monkeypatch.setenv("MOE_GEMM_PAIRS", pairs)
+    case = _case([200, 90], 384, 32768, gather, seed=6, T=250)   # an epilogue waits for 128 stages
+    monkeypatch.setenv("MOE_WAIT_LIMIT_CYCLES", "1")
+    _, e = _product(case)
+    assert e == TIMEOUT
+    monkeypatch.delenv("MOE_WAIT_LIMIT_CYCLES")
+    _check_product(case)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("lens,gather", [([5, 40, 3], False), ([150, 260], True)])
 def test_product_rows_behind_and_determinism(lens, gather):
     """Rows past the last segment come out zero, rows past M_alloc stay; two runs give the same bits."""
@@ -298,6 +352,39 @@ def test_product_graph_on_two_streams():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], _product(second[:2] + cases[0][2:4] + second[4:])[0])
+
+
+@pytest.mark.gpu
+@pytest.mark.slow
+def test_rows_past_32_bits_of_elements():
+    """Codes, outputs and quantised values whose offsets pass 2^31 elements: the last rows against 64 bits."""
+    K, N, M = 1024, 32768, 70000                      # out: 2.3e9 values
+    row = torch.randn(M, K, device="cuda").bfloat16()
+    codes, scales, _ = m.moe_quantize_mxfp4(row)
+    wt = torch.randn(N, K, device="cuda").bfloat16()
+    wc, wsc, _ = m.moe_quantize_mxfp4(wt)
+    w = m.moe_prepare_weights(m.Weight("mxfp4", wc.view(1, N, -1), wsc.view(1, N, -1)))
+    out = m.moe_grouped_gemm_mxfp4(codes, scales, w, torch.tensor([M], dtype=torch.int32, device="cuda"))
+    u = lambda t: t.cpu().numpy()
+    for r in (0, 65535, 65536, M - 1):
+        a = O.mxfp4_dequantize_rows(O.unpack_e2m1(u(codes[r:r + 1])), u(scales[r:r + 1]))[0]
+        wv = O.mxfp4_dequantize_rows(O.unpack_e2m1(u(wc[-256:])), u(wsc[-256:]))
+        ref, mag = wv @ a, np.abs(wv) @ np.abs(a)
+        slack = (K / 64 + 1) * 2.0 ** -22 * mag
+        assert np.all(np.abs(out[r, -256:].double().cpu().numpy() - ref) <= slack + (np.abs(ref) + slack) * 2.0 ** -8)
+    del out, row, codes
+    R, K = 300000, 8192                               # 2.5e9 values in
+    x = torch.randn(1, K, device="cuda").bfloat16().repeat(R, 1)
+    x[-1] *= 3
+    c, s, d = m.moe_quantize_mxfp4(x, deq=True)
+    for r in (0, R - 2, R - 1):
+        rc, rs = O.mxfp4_quantize_rows(x[r:r + 1].float().cpu().numpy())
+        assert np.array_equal(u(c[r:r + 1]), _pack(rc)) and np.array_equal(u(s[r:r + 1]), rs)
+        assert np.array_equal(d[r:r + 1].double().cpu().numpy(), O.mxfp4_dequantize_rows(rc, rs))
+    n = m.moe_add_rmsnorm(x, quant="mxfp4")
+    assert torch.equal(n["codes"][0], n["codes"][R - 2])
+    _, y = O.add_rmsnorm(x[-1:].double().cpu().numpy())
+    assert np.all(np.abs(n["y"][-1:].double().cpu().numpy() - y) <= np.abs(y) * (2.0 ** -8 + 1e-5) + 1e-38)
 
 
 # ------------------------------------------------------------------ together (GPU)

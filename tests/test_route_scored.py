@@ -191,3 +191,37 @@ def test_graph_and_streams():
     g.replay()
     torch.cuda.synchronize()
     assert np.array_equal(ids.cpu().numpy(), O.route_scored(x.cpu().numpy(), 4)[0])
+
+
+@pytest.mark.gpu
+@pytest.mark.slow
+def test_logits_past_32_bits_of_elements():
+    T, E = 2 ** 31 // 1024 + 50, 1024                 # 4.3 GB of bf16 logits
+    x = torch.randn(1, E, device="cuda").bfloat16().repeat(T, 1)
+    x[-1] = torch.randn(E).bfloat16()
+    ids, w = m.moe_route_scored(x, 8)
+    for r in (0, T - 2, T - 1):
+        rids, rw = O.route_scored(x[r:r + 1].double().cpu().numpy(), 8)
+        assert np.array_equal(ids[r:r + 1].cpu().numpy(), rids)
+        assert np.allclose(w[r:r + 1].cpu().numpy(), rw, rtol=1e-5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,ng", [(256, 8), (160, 8), (1024, 32), (48, 4), (96, 1), (24, 1)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_close_scores_are_decided_in_64_bits(E, ng, scoring):
+    """Rows made of few distinct logits a last place apart, biases that nearly cancel the difference of
+    the scores: neighbours and group sums within the error of 32 bits, in runs shorter and longer than
+    the 32 candidates that are ordered at once."""
+    g = torch.Generator().manual_seed(E)
+    base = torch.tensor([0.5, 1.0, 1.5])
+    x = base[torch.randint(0, 3, (120, E), generator=g)]
+    x = x + torch.randint(-2, 3, (120, E), generator=g) * 2.0 ** -23
+    b = torch.randint(-3, 4, (E,), generator=g) * 2.0 ** -24
+    k = min(8, E // ng * max(1, ng // 2))
+    for gscore in ("max", "top2"):
+        _check(x, k, scoring, b, ng, max(1, ng // 2), gscore, True, 1.0)
+        _check(x, k, scoring, None, ng, max(1, ng // 2), gscore, False, 1.0)
+    wide = torch.randn(E, generator=g)                # every expert live, c within a few places of each other
+    s = torch.sigmoid(wide.double()) if scoring == "sigmoid" else torch.softmax(wide.double(), 0)
+    _check(wide.expand(40, E).contiguous(), k, scoring, (0.75 - s).float(), ng, max(1, ng // 2), "top2", True, 1.0)
