@@ -155,6 +155,7 @@ moe_status_t moe_route_topk_grouped(const float* logits, const float* bias, int 
  *   topk_ids int32 / topk_w fp32 [T,topk] out, dense.
  * E % n_group, 1 <= topk_group <= n_group, 1 <= topk <= topk_group*E/n_group and a finite
  * positive scaling factor, else INVALID_ARG; E > 1024, n_group > 32 or topk > 32: UNSUPPORTED.
+ * Pointers need their element's alignment only (else MOE_ERR_ALIGNMENT).
  */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
 typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score_t;
@@ -430,7 +431,8 @@ moe_status_t moe_quantize_mxfp4(const void* in, int in_is_f32, int64_t in_stride
  *   w       MXFP4 weights prepared by moe_prepare_weights (else NOT_PREPARED); other formats:
  *           UNSUPPORTED.
  *   out bf16 [M_alloc, N], N % 8 == 0; cu_seqlens int32 [G] on device; G <= 1024.
- *   ws: at least 256 bytes (the error word).
+ *   ws: at least 256 bytes (the error word). The first call on a device sets kernel attributes:
+ *   make it before any stream capture.
  */
 moe_status_t moe_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int a_rows,
                                     const int32_t* row_idx, int M_alloc, const moe_weight_t* w,

@@ -231,6 +231,9 @@ moe_status_t moe_route_scored(const moe_route_args_t* p, moe_stream_t stream) {
     if (p->E > kMaxExperts || p->n_group > 32 || p->topk > kMaxTopk) return MOE_ERR_UNSUPPORTED;
     if (p->T == 0) return MOE_OK;
     if (!p->logits || !p->topk_ids || !p->topk_w) return MOE_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(p->logits) % (p->in_is_bf16 ? 2 : 4) || reinterpret_cast<uintptr_t>(p->bias) % 4 ||
+        reinterpret_cast<uintptr_t>(p->topk_ids) % 4 || reinterpret_cast<uintptr_t>(p->topk_w) % 4)
+        return MOE_ERR_ALIGNMENT;
     return cuda_status(launch_route_scored(*p, S(stream), false));
 }
 

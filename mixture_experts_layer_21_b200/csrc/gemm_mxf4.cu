@@ -23,8 +23,8 @@
 // shared and tensor memory is not in line with the codes' copies. Warp roles, each run by whole warps
 // with one lane elected to issue:
 //   producer   the codes of both sides into the stages (tokens only in segment order)
-//   MMA        one issuer, or two with partial sums of their own
-//   copiers    two: scale blocks from the scale ring into tensor-memory slots
+//   MMA        the issuer
+//   copier     scale blocks from the scale ring into tensor-memory slots
 //   epilogue   four warps: tensor memory -> alpha, bf16 -> out
 //   scales     four warps, taking the stages in turn: both sides' scale blocks into the scale ring
 //   gather     four warps, likewise (with row_idx): the token rows' codes by cp.async
@@ -48,7 +48,6 @@ namespace {
 constexpr int kStageK = 256;
 constexpr int kScaleWarps = 4;
 constexpr int kGatherWarps = 4;
-constexpr int kCopiers = 1;
 constexpr int kSfRing = 8;
 
 // Tiles whose rows the producer may have written and the MMA issuers not yet read: it is at most
@@ -98,11 +97,8 @@ struct Mxf4Cfg {
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int RG = (BT + 127) / 128;                 // 128-row groups of the token side
     static constexpr int SF_ENTRY = 1024 + 2 * RG * 512;        // weights' two blocks, tokens' [128-K half][row group]
-    // A thread issues block-scaled MMAs one after the other, each about 110 cycles however narrow, so
-    // narrow tiles split each stage's four K steps between two issuers with partial sums of their own.
-    static constexpr int NI = BT <= 64 ? 2 : 1;
     static constexpr int SF_SLOT = 8 + 8 * RG;                  // TMEM columns of a stage's scales
-    static constexpr int SF_BASE = 2 * NI * BT;                 // after two accumulators
+    static constexpr int SF_BASE = 2 * BT;                      // after two accumulators
     static constexpr int SLOTS = cmin(kSfRing, (512 - SF_BASE) / SF_SLOT);
     static constexpr int TMEM_COLS = tmem_cols_pow2(SF_BASE + SLOTS * SF_SLOT);
     // behind the stages: the scale ring, the control block, the gather warps' row tables, the epilogue's staging
@@ -111,13 +107,13 @@ struct Mxf4Cfg {
     static constexpr int TAIL_BYTES = kSfRing * SF_ENTRY + STAGING_OFF + 4 * 2048;
     static constexpr int STAGES = cmin(kMaxStages, (kSmemLimit - 1024 - TAIL_BYTES) / STAGE);
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE + TAIL_BYTES;
-    static constexpr int COPIER_WARP0 = 1 + NI;
-    static constexpr int EPI_WARP0 = COPIER_WARP0 + kCopiers;
+    static constexpr int COPIER_WARP = 2;
+    static constexpr int EPI_WARP0 = COPIER_WARP + 1;
     static constexpr int SCALE_WARP0 = EPI_WARP0 + 4;
     static constexpr int GATHER_WARP0 = SCALE_WARP0 + kScaleWarps;
     static constexpr int THREADS = (GATHER_WARP0 + (GATHER ? kGatherWarps : 0)) * 32;
     static_assert(BT % 16 == 0 && BT >= 16 && BT <= 240, "token tile");
-    static_assert(!PAIR || (BT % 32 == 0 && NI == 1), "pair MMA N: a multiple of 32");
+    static_assert(!PAIR || BT % 32 == 0, "pair MMA N: a multiple of 32");
     static_assert(STAGES >= 3 && SLOTS >= 2 && SMEM_BYTES <= kSmemLimit && SF_BASE + SLOTS * SF_SLOT <= 512, "MXFP4 GEMM config");
     static_assert(B_BYTES % 1024 == 0, "operand alignment");
 };
@@ -194,7 +190,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&ctl->full[s], 1);
-            mbar_init(&ctl->empty[s], C::NI);
+            mbar_init(&ctl->empty[s], 1);
             mbar_init(&mc->gfull[s], 32);  // the lanes of the gather warp that copied the stage's rows
             mbar_init(&pfull[s], 1);
         }
@@ -203,13 +199,13 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             mbar_init(&mc->psf[d], 1);
             mbar_init(&mc->sf_free[d], 1);
             mbar_init(&mc->sf_full[d], 1);
-            mbar_init(&mc->slot_free[d], C::NI);
+            mbar_init(&mc->slot_free[d], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&ctl->tfull[b], C::NI);
+            mbar_init(&ctl->tfull[b], 1);
             mbar_init(&ctl->tempty[b], PAIR ? 8 : 4);
         }
-        for (int i = 0; i < C::NI + kCopiers; ++i) mbar_init(&ctl->drain[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&ctl->drain[i], 1);
         ctl->abort = 0;
         fence_barrier_init();
     }
@@ -287,10 +283,9 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             }
         }
         if (!ok) give_up(1);
-    } else if (warp < C::COPIER_WARP0) {
-        // ---------------- MMAs: issuer I takes its share of each stage's four K steps
-        auto issue = [&](auto first) {
-            constexpr int SHARE = 4 / C::NI, I = decltype(first)::value;
+    } else if (warp == 1) {
+        // ---------------- MMAs
+        if (leader) {
             const uint64_t a0 = sw128_kmajor_desc(smem_u32(opA(0))), b0 = sw128_kmajor_desc(smem_u32(opB(0)));
             constexpr uint32_t id2 = idesc_mxf4(0, 0, 2) ^ idesc_mxf4(0, 0, 0), at2 = 2u << 30;
             Ring st, sl;
@@ -302,7 +297,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                     ok = false;
                     break;
                 }
-                const uint32_t d = tmem_base + (uint32_t)((b * C::NI + I) * BT);
+                const uint32_t d = tmem_base + (uint32_t)(b * BT);
                 for (int kb = 0; kb < KB; ++kb) {
                     if ((!next_sf && !wait(&mc->sf_full[sl.i], sl.ph)) || (!next_full && !wait(&ctl->full[st.i], st.ph)) ||
                         (!next_g && !wait(&mc->gfull[st.i], st.ph)) ||
@@ -327,12 +322,11 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                     const int steps = (a.K - kb * kStageK + 63) >> 6;
                     if (elect_one()) {
 #pragma unroll
-                        for (int i = 0; i < SHARE; ++i) {
-                            const int j = I * SHARE + i;
+                        for (int j = 0; j < 4; ++j) {
                             if (j < steps) {
                                 const uint32_t id = j & 1 ? idesc | id2 : idesc, at = j & 1 ? at2 : 0u;
                                 const uint32_t fa = (sfa + 4 * (j >> 1)) | at, fb = (sfa + 8 + 4 * C::RG * (j >> 1)) | at;
-                                const uint32_t acc = i ? 1u : (uint32_t)(kb != 0);
+                                const uint32_t acc = j ? 1u : (uint32_t)(kb != 0);
                                 if (PAIR) mma_mxf4_ss_pair(d, as + 2 * j, bs + 2 * j, id, fa, fb, acc);
                                 else mma_mxf4_ss(d, as + 2 * j, bs + 2 * j, id, fa, fb, acc);
                             }
@@ -351,11 +345,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                 if (b == 0) bph ^= 1u;
             }
             if (!ok) give_up(2);
-        };
-        if (leader) {
-            if (warp == 1) issue(std::integral_constant<int, 0>{});
-            else issue(std::integral_constant<int, C::NI - 1>{});
-        } else if (GATHER && warp == 1) {
+        } else if (GATHER) {
             // peer: tells the leader that its gathered rows of each stage landed
             Ring st;
             bool ok = true;
@@ -373,49 +363,45 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             }
             if (!ok) give_up(6);
         }
-    } else if (warp < C::EPI_WARP0) {
+    } else if (warp == C::COPIER_WARP) {
         // ---------------- scale blocks: ring -> tensor memory (peer: tells the leader they are in its
-        // ring); the copiers take the stages in turn
+        // ring)
         const uint64_t ring0 = sf_block_desc(smem_u32(sf_ring));
-        const int mine = warp - C::COPIER_WARP0;
-        int it = 0;
         Ring rg, sl;
         bool ok = true;
         for (int L = first_tile; L < total && ok; L += tile_step) {
             int g, nt, row0, rows;
             tile(L, g, nt, row0, rows);
             const bool wide = C::RG > 1 && mma_n(rows) > 128;  // the second 128-row group is in use
-            for (int kb = 0; kb < KB; ++kb, ++it) {
-                if (it % kCopiers == mine) {
-                    if (!wait(&mc->sf_ready[rg.i], rg.ph) ||
-                        (leader && ((PAIR && !wait(&mc->psf[rg.i], rg.ph)) || !wait(&mc->slot_free[sl.i], sl.ph ^ 1u)))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t src = ring0 + (uint64_t)(rg.i * (C::SF_ENTRY >> 4));
-                    const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + sl.i * C::SF_SLOT), sfb = sfa + 8;
-                    const bool both = a.KS - 2 * kb > 1;  // both 128-K halves
-                    auto copy = [](uint32_t t, uint64_t desc) {
-                        if (PAIR) tmem_cp_32x128b_x4_pair(t, desc);
-                        else tmem_cp_32x128b_x4(t, desc);
-                    };
-                    if (elect_one()) {
-                        if (!leader) {
-                            mbar_arrive_remote(mapa_shared(smem_u32(&mc->psf[rg.i]), 0));
-                        } else {
+            for (int kb = 0; kb < KB; ++kb) {
+                if (!wait(&mc->sf_ready[rg.i], rg.ph) ||
+                    (leader && ((PAIR && !wait(&mc->psf[rg.i], rg.ph)) || !wait(&mc->slot_free[sl.i], sl.ph ^ 1u)))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t src = ring0 + (uint64_t)(rg.i * (C::SF_ENTRY >> 4));
+                const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + sl.i * C::SF_SLOT), sfb = sfa + 8;
+                const bool both = a.KS - 2 * kb > 1;  // both 128-K halves
+                auto copy = [](uint32_t t, uint64_t desc) {
+                    if (PAIR) tmem_cp_32x128b_x4_pair(t, desc);
+                    else tmem_cp_32x128b_x4(t, desc);
+                };
+                if (elect_one()) {
+                    if (!leader) {
+                        mbar_arrive_remote(mapa_shared(smem_u32(&mc->psf[rg.i]), 0));
+                    } else {
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                if (h == 0 || both) {
-                                    copy(sfa + 4 * h, src + 32 * h);
-                                    copy(sfb + 4 * h * C::RG, src + 64 + 32 * h * C::RG);
-                                    if (wide) copy(sfb + 4 * (h * C::RG + 1), src + 64 + 32 * (h * C::RG + 1));
-                                }
+                        for (int h = 0; h < 2; ++h) {
+                            if (h == 0 || both) {
+                                copy(sfa + 4 * h, src + 32 * h);
+                                copy(sfb + 4 * h * C::RG, src + 64 + 32 * h * C::RG);
+                                if (wide) copy(sfb + 4 * (h * C::RG + 1), src + 64 + 32 * (h * C::RG + 1));
                             }
-                            is.tc = true;
-                            commit_here(&mc->sf_full[sl.i]);
-                            commit(&mc->sf_free[rg.i]);
                         }
+                        is.tc = true;
+                        commit_here(&mc->sf_full[sl.i]);
+                        commit(&mc->sf_free[rg.i]);
                     }
                 }
                 rg.next(kSfRing);
@@ -445,10 +431,9 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                 break;
             }
             tc_fence_after();
-            const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::NI * BT);
+            const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BT);
             const int n0 = (PAIR ? 2 * nt + rank : nt) * kTileN + q * 32;
             const float al = a.alpha ? a.alpha[g] : 1.0f;
-            const bool two = C::NI == 2 && a.K > kStageK / 2;  // the second issuer has sums (not for half a stage)
 #pragma unroll 1
             for (int c0 = 0; c0 < rows; c0 += 32) {
                 const bool more = c0 + 16 < rows;  // the MMA wrote rows rounded up to 16
@@ -457,19 +442,6 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                 for (int i = 0; i < 4; ++i)
                     if (i < 2 || more) tmem_ld_16x16(tb + c0 + 16 * (i >> 1) + ((uint32_t)(16 * (i & 1)) << 16), r[i]);
                 tmem_ld_wait();
-                if (two) {
-                    uint32_t r1[4][8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i < 2 || more)
-                            tmem_ld_16x16(tb + BT + c0 + 16 * (i >> 1) + ((uint32_t)(16 * (i & 1)) << 16), r1[i]);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            r[i][j] = __float_as_uint(__uint_as_float(r[i][j]) + __uint_as_float(r1[i][j]));
-                }
                 __syncwarp();  // the previous chunk has been read
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {

@@ -229,7 +229,7 @@ cudaError_t run_rmsnorm(const moe_rmsnorm_args_t& a, cudaStream_t st, bool pdl) 
     // a block to a row 39).
     const int chunks = a.H / 8;
     const bool many = a.T >= 2 * num_sms();
-    if (many && chunks <= 64) return run_rmsnorm<2, F32, true>(a, dim3((a.T + 7) / 8), dim3(32, 8), st, pdl);
+    if (many && chunks <= 64) return run_rmsnorm<2, F32, true>(a, dim3((a.T - 1) / 8 + 1), dim3(32, 8), st, pdl);
     const int cpt = chunks > 2048 ? 4 : many || chunks > 1024 ? 2 : 1;
     const dim3 grid(a.T), block(((chunks + cpt - 1) / cpt + 31) / 32 * 32);
     if (cpt == 1) return run_rmsnorm<1, F32>(a, grid, block, st, pdl);

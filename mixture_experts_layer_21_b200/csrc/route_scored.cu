@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(128) route_scored_kernel(const moe_route_args_
 
 template <int EPL, bool BF16>
 cudaError_t run_route(const moe_route_args_t& r, cudaStream_t st, bool pdl) {
-    const dim3 grid((r.T + 3) / 4), block(128);
+    const dim3 grid((r.T - 1) / 4 + 1), block(128);
     const int bytes = BF16 ? 2 : 4;
     const size_t smem = 4 * sizeof(double) * 32 * EPL;  // at most 32 KB
     RoutePlan p{};

@@ -17,7 +17,7 @@ import mixture_experts_layer_21_b200 as m
 from oracle import moe_oracle as O
 
 L = m.lib()
-INVALID, UNSUP = 1, 2
+INVALID, UNSUP, ALIGN = 1, 2, 3
 
 
 def _call(**kw):
@@ -38,6 +38,12 @@ def _call(**kw):
                                 dict(logits=None), dict(topk_ids=None), dict(topk_w=None)])
 def test_refuses_bad_arguments(kw):
     assert _call(**kw) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(logits=18), dict(logits=17, in_is_bf16=1), dict(bias=2), dict(topk_ids=18),
+                                dict(topk_w=17)])
+def test_refuses_misaligned_pointers(kw):
+    assert _call(**kw) == ALIGN
 
 
 @pytest.mark.parametrize("kw", [dict(E=1025), dict(E=66, n_group=33, topk_group=33), dict(E=64, topk=33)])
