@@ -153,6 +153,16 @@ __global__ void __launch_bounds__(256) quant_mxfp4_kernel(const void* in, long l
     pdl_launch();
 }
 
+// 1 / sqrt(m), rounded once to fp32: fp32's value and one Newton step in fp64. The factor goes into
+// every value of a row, and an error in it moves codes of the row across their rounding borders, all
+// in one direction; with fp32 throughout 8192 rows of 7168 had twice the codes off that the two
+// roundings of the products cost.
+MOE_DEV float inv_sqrt(double m) {
+    const float f = rsqrtf((float)m);
+    const double r = (double)f;
+    return f == 0.0f ? 0.0f : (float)(r * (1.5 - 0.5 * m * r * r));  // 0: an infinite m
+}
+
 // A block to a row (SHORT: a warp, blockDim.y of them to a block); thread t holds chunks t, t + blockDim.x of
 // eight values in registers, so the row is read once. What bounds long inputs is the memory traffic in
 // flight between the rows' barriers: the registers are held to 32 a thread, 2048 threads an SM (8192
@@ -189,13 +199,14 @@ __global__ void __launch_bounds__(1024, CPT <= 2 ? 2 : 1) add_rmsnorm_kernel(con
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    double total = sum;
     if (!SHORT) {
         if (lane_id() == 0) part[warp_id()] = sum;
         __syncthreads();
-        sum = 0.0f;
-        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) sum += part[w];
+        total = 0.0;
+        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) total += part[w];
     }
-    const float rstd = 1.0f / sqrtf(sum / (float)a.H + a.eps);
+    const float rstd = inv_sqrt(total * (1.0 / a.H) + a.eps);
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
