@@ -139,8 +139,9 @@ moe_status_t moe_route_topk_grouped(const float* logits, const float* bias, int 
  * steers the selection of softmax scores, whose groups are ranked by their best expert, whose
  * weights are not renormalised, or whose logits are bf16, strided or masked.
  *   s_e = softmax(l)_e (MOE_SCORE_SOFTMAX) or sigmoid(l_e) (MOE_SCORE_SIGMOID);
- *   c_e = s_e + bias_e. bias (fp32 [E], finite, NULL = 0) steers the selection only. Without
- *   a bias the experts are ranked by their logits, of which s is an increasing function.
+ *   c_e = s_e + bias_e. bias (fp32 [E], NULL = 0) steers the selection only; one of -inf or NaN
+ *   ranks its expert with the masked ones below, its s unchanged. Without a bias the experts
+ *   are ranked by their logits, of which s is an increasing function.
  *   The E experts form n_group consecutive groups. A group scores its largest c
  *   (MOE_GROUP_MAX) or the sum of its two largest (MOE_GROUP_TOP2; its one c where it has one
  *   live expert). The topk_group best groups are kept, ties to the lower group. The topk

@@ -5,7 +5,8 @@
 // are one wide load.
 //
 // A masked expert (logit -inf or NaN) has s = 0 and ranks below every live one of the kept
-// groups, by id among its like, so that the ids a row gets are always valid and distinct.
+// groups, by id among its like, so that the ids a row gets are always valid and distinct. One
+// whose bias is -inf or NaN ranks with them.
 //
 // The decisions are those of fp64. The scores are computed in fp32 first, with a bound on their
 // error, and where every comparison that decides is wider than it (but for a token in some
@@ -53,8 +54,9 @@ struct Token64 {
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         norm = a.scoring == MOE_SCORE_SIGMOID || !(sum > 0.0) ? 1.0 : sum;
     }
-    MOE_DEV double value(int e, float l, double p) const {  // c, -inf where masked
-        return l == -INFINITY ? -(double)INFINITY : p / norm + (a.bias ? (double)a.bias[e] : 0.0);
+    MOE_DEV double value(int e, float l, double p) const {  // c, -inf where masked; never NaN
+        const float b = a.bias ? a.bias[e] : 0.0f;
+        return l == -INFINITY || isnan(b) ? -(double)INFINITY : p / norm + (double)b;
     }
 };
 
@@ -324,7 +326,8 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             bmax = fmaxf(bmax, fabsf(b[i]));
-            key[i] = order_key(l[i] > -INFINITY ? s[i] + b[i] : -INFINITY);
+            const float c = s[i] + b[i];
+            key[i] = order_key(l[i] > -INFINITY && c > -INFINITY ? c : -INFINITY);  // NaN as -inf
         }
     } else {
 #pragma unroll
@@ -335,7 +338,17 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
         for (int i = 0; i < EPL; ++i)
             if (i >= live) key[i] = 0u;
     }
-    if (a.bias) bmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
+    if (a.bias) {
+        bmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
+        if (bmax == INFINITY) {  // the largest finite one: an infinite sum has no error
+            bmax = 0.0f;
+            for (int i = 0; i < live; ++i) {
+                const float f = fabsf(__ldg(a.bias + lane * EPL + i));
+                if (f < INFINITY) bmax = fmaxf(bmax, f);
+            }
+            bmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
+        }
+    }
     if (GROUPS) {
         const int gs = plan.gs;
         // each group's two largest keys of c (of s without a bias; of the logits where the best expert

@@ -250,7 +250,8 @@ def route_scored(logits, topk: int, scoring: str = "softmax", bias=None, n_group
                  group_score: str = "max", renormalize: bool = True, routed_scaling_factor: float = 1.0):
     """Routing by scores, token by token in fp64.
 
-      s = softmax(l) or sigmoid(l), 0 for a masked expert (logit -inf or NaN); c = s + bias.
+      s = softmax(l) or sigmoid(l), 0 for a masked expert (logit -inf or NaN); c = s + bias, -inf for
+      a masked expert and one whose bias is NaN.
       Live experts rank by c (without a bias, by their logits), then by id; masked ones follow by id.
       A group scores the largest c of its live experts, or the sum of up to two largest ("top2");
       one without a live expert scores -inf. The topk_group best groups are kept (ties to the lower
@@ -274,7 +275,7 @@ def route_scored(logits, topk: int, scoring: str = "softmax", bias=None, n_group
             with np.errstate(invalid="ignore"):      # +inf logits share the weight equally
                 z = np.where(l == l.max(), 1.0, np.exp(l - l.max()))
             s = np.where(live, z / z.sum(), 0.0) if live.any() else np.zeros(E)
-        c = np.where(live, s + b, -np.inf)
+        c = np.where(live & ~np.isnan(b), s + np.where(np.isnan(b), 0.0, b), -np.inf)
         key = l if bias is None else c
         gkey = key if bias is None and group_score == "max" else c
         score = np.full(n_group, -np.inf)

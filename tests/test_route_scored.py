@@ -164,6 +164,43 @@ def test_masked_experts(scoring, ng, tg, gscore, bias):
     _check(x, 6, scoring, b, ng, tg, gscore, False, 1.5)
 
 
+def test_oracle_biases_that_are_not_finite():
+    x = np.array([[0.0, 1.0, 2.0, 3.0]])
+    b = np.array([np.nan, 0.5, -np.inf, -np.inf])
+    assert O.route_scored(x, 4, "sigmoid", b)[0].tolist() == [[1, 0, 2, 3]]
+    assert O.route_scored(x, 2, "sigmoid", np.array([0.0, np.inf, 0.0, np.inf]))[0].tolist() == [[1, 3]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,ng,tg", [(64, 1, 1), (64, 4, 2), (256, 8, 4), (36, 6, 2)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("gscore", ["max", "top2"])
+def test_biases_that_are_not_finite(E, ng, tg, scoring, gscore):
+    """-inf and NaN of either sign rank an expert with the masked ones, +inf before all others: some
+    experts, a whole group, all but fewer than topk, all."""
+    g = torch.Generator().manual_seed(E + ng)
+    x = torch.randn(40, E, generator=g)
+    x[1] = float("-inf")
+    x[2, ::3] = float("nan")
+    nan = torch.tensor([0x7fc00000, -0x400000], dtype=torch.int32).view(torch.float32)
+    for kind in range(5):
+        b = torch.randn(E, generator=g) * 0.1
+        if kind == 0:
+            b[torch.rand(E, generator=g) < 0.3] = float("-inf")
+            b[::7], b[1::7] = nan[0], nan[1]
+        elif kind == 1:
+            b[:E // ng] = float("-inf") if ng > 1 else float("nan")
+        elif kind == 2:
+            b[2:] = nan[1]
+        elif kind == 3:
+            b[:] = nan[0]
+        else:
+            b[5::6] = float("inf")
+            b[::5] = float("-inf")
+        _check(x, 6, scoring, b, ng, tg, gscore, True, 1.0)
+        _check(x, 6, scoring, b, ng, tg, gscore, False, 1.5)
+
+
 @pytest.mark.gpu
 def test_large_and_close_scores():
     """Saturated sigmoids, logits far apart, and sums s + b that differ by a few 2^-25."""
