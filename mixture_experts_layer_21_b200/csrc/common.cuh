@@ -417,9 +417,9 @@ MOE_DEV uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 MOE_DEV void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// The same without a release at cluster scope, which waits until every store of this thread, and it
-// seems of the SM, is visible to the cluster (about 1000 cycles under a storing epilogue): for
-// arrivals that announce what the tensor cores read or wrote, ordered by their own fences.
+// The same without a release at cluster scope, which waits until every earlier store is visible to the
+// cluster (measured: about 1000 cycles while the epilogue stores): for arrivals that announce what the
+// tensor cores read or wrote, ordered by their own fences.
 MOE_DEV void mbar_arrive_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

@@ -10,10 +10,10 @@
 // A pipeline stage is 256 values of K: 128 bytes of packed codes per row on either side, in the
 // 128-byte swizzle, and the stage's scales as 512-byte blocks in tensor-memory copy order. The
 // weights come by TMA, and so do token rows in segment order. Token rows that row_idx gathers come
-// by cp.async from the token warps: the four-row TMA gather took about 80 cycles a copy, 1.15 ms
+// by cp.async from the gather warps: the four-row TMA gather took about 80 cycles a copy, 1.15 ms
 // against 0.30 ms in segment order for 8192 rows x 4096 into 14336. The weights' scales are
 // prepared blocks; the tokens' [rows, K/32] bytes may sit at any alignment, which no TMA copy
-// takes, so the token warps load them through registers.
+// takes, so the scale warps load them through registers.
 //
 // PAIR: two SMs per tile (a cluster of two CTAs, cta_group::2). A pair tile is 256 weight rows, 128
 // from each CTA's shared memory, by up to BT tokens, half of them from each, so an SM moves half the
@@ -23,7 +23,7 @@
 // shared and tensor memory is not in line with the codes' copies. Warp roles, each run by whole warps
 // with one lane elected to issue:
 //   producer   the codes of both sides into the stages (tokens only in segment order)
-//   MMA        the issuer
+//   MMA        a stage's four instructions at most
 //   copier     scale blocks from the scale ring into tensor-memory slots
 //   epilogue   four warps: tensor memory -> alpha, bf16 -> out
 //   scales     four warps, taking the stages in turn: both sides' scale blocks into the scale ring
@@ -37,7 +37,6 @@
 //   sf_full[t]   the scales are in tensor memory;  slot_free[t]  their MMAs completed
 //   tfull[b]     accumulator b holds a finished tile (both CTAs);  tempty[b]  it was read (leader)
 #include <cmath>
-#include <type_traits>
 
 #include "gemm_common.cuh"
 
@@ -50,8 +49,8 @@ constexpr int kScaleWarps = 4;
 constexpr int kGatherWarps = 4;
 constexpr int kSfRing = 8;
 
-// Tiles whose rows the producer may have written and the MMA issuers not yet read: it is at most
-// kMaxStages stages, so at most as many tiles, ahead of the slowest of them.
+// Tiles whose rows the producer may have written and the MMA warp not yet read: it is at most
+// kMaxStages stages, so at most as many tiles, ahead.
 constexpr int kTileRing = 32;
 
 // The control block with what only this kernel has.
@@ -116,6 +115,8 @@ struct Mxf4Cfg {
     static_assert(!PAIR || BT % 32 == 0, "pair MMA N: a multiple of 32");
     static_assert(STAGES >= 3 && SLOTS >= 2 && SMEM_BYTES <= kSmemLimit && SF_BASE + SLOTS * SF_SLOT <= 512, "MXFP4 GEMM config");
     static_assert(B_BYTES % 1024 == 0, "operand alignment");
+    // a warp that takes every n-th turn of a ring finds the turn of an entry before its own finished
+    static_assert((!GATHER || STAGES >= kGatherWarps) && kSfRing % kScaleWarps == 0, "turns of the rings");
 };
 
 MOE_DEV uint4 ld_shared16(uint32_t addr) {
@@ -364,8 +365,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             if (!ok) give_up(6);
         }
     } else if (warp == C::COPIER_WARP) {
-        // ---------------- scale blocks: ring -> tensor memory (peer: tells the leader they are in its
-        // ring)
+        // ---------------- scale blocks: ring -> tensor memory (peer: tells the leader they are in its ring)
         const uint64_t ring0 = sf_block_desc(smem_u32(sf_ring));
         Ring rg, sl;
         bool ok = true;
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
         // A warp's 32 weight rows of 32 tokens are transposed through its own 2 KB of shared memory (64
         // bytes a token, the 16-byte pieces of token t at c ^ (t / 2 % 4) against bank conflicts), so that
         // a store writes 64 contiguous bytes of eight tokens. Stores of two bytes a lane straight from
-        // the registers held the kernel at 228 us in the case above without any loads or MMAs.
+        // the registers held the kernel at 228 us in the 14336 x 4096 case without any loads or MMAs.
         const int q = warp & 3;
         const uint32_t stage = smem_u32(mc) + C::STAGING_OFF + q * 2048;
         // stmatrix: lane 8 i + k addresses token k + 8 (i / 2), 16-byte piece (i % 2) + 2 (row half)
