@@ -211,10 +211,11 @@ __device__ __noinline__ void route64(const moe_route_args_t& a, int t, double* c
 
 // ----------------------------------------------------------------- fp32
 // The order of floats as unsigned integers; 0 is below -inf.
-MOE_DEV uint32_t order_key(float f) {
-    const uint32_t u = __float_as_uint(f + 0.0f);  // -0 as +0
+MOE_DEV uint32_t order_bits(float f) {
+    const uint32_t u = __float_as_uint(f);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
+MOE_DEV uint32_t order_key(float f) { return order_bits(f + 0.0f); }  // -0 as +0
 MOE_DEV float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
 // Keys in descending order, by Batcher's odd-even merge sort (K. E. Batcher, Sorting networks and their
@@ -257,7 +258,8 @@ struct RoutePlan {
 
 // One token, in fp32 where that decides. False where it cannot (infinite logits, more than 32
 // candidates within the error of each other); nothing is written then. What bounds it is the number
-// of instructions (about 700 a token with 256 experts in 8 groups, at 1600 36 us for 16384 tokens).
+// of instructions (1046 a token with 256 experts in 8 groups, 27 us for 16384 tokens; at 1260 30 us, at
+// 1600 36).
 //
 // Error of the scores that rank. Sigmoid: the exponential's argument -l log2(e) rounds twice, 2^-23 |l|
 // relative to the exponential e, whose approximation is within 2^-22; e / (1 + e)^2 <= 1/4 and |l| e / (1 + e)^2
@@ -285,12 +287,15 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
     // scores of every expert, where the selection, the groups or the raw softmax weights need them
     const bool top2 = GROUPS && a.group_score == MOE_GROUP_TOP2;
     const bool raw = softmax && !a.renormalize;
+    auto approx = [&](float x) {  // softmax: without its denominator; 0 where masked
+        return softmax ? exp2_approx((x - mx) * LOG2E) : rcp_approx(1.0f + exp2_approx(x * -LOG2E));
+    };
     if (a.bias || raw || top2) {
         if (softmax) {
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
-                s[i] = raw ? expf(l[i] - mx) : exp2_approx((l[i] - mx) * LOG2E);  // 0 where masked
+                s[i] = raw ? expf(l[i] - mx) : approx(l[i]);
                 sum += s[i];
             }
 #pragma unroll
@@ -298,9 +303,9 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
             inv = 1.0f / sum;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) s[i] *= inv;
-        } else {
+        } else if (a.bias) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) s[i] = rcp_approx(1.0f + exp2_approx(l[i] * -LOG2E));
+            for (int i = 0; i < EPL; ++i) s[i] = approx(l[i]);
         }
     }
     // what ranks the experts, as order keys: c, or the logits; below them masked experts (-inf),
@@ -326,8 +331,8 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             bmax = fmaxf(bmax, fabsf(b[i]));
-            const float c = s[i] + b[i];
-            key[i] = order_key(l[i] > -INFINITY && c > -INFINITY ? c : -INFINITY);  // NaN as -inf
+            const float c = s[i] + b[i];  // not -0: s is not
+            key[i] = order_bits(l[i] > -INFINITY && c > -INFINITY ? c : -INFINITY);  // NaN as -inf
         }
     } else {
 #pragma unroll
@@ -349,48 +354,54 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
             bmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
         }
     }
-    if (GROUPS) {
-        const int gs = plan.gs;
-        // each group's two largest keys of c (of s without a bias; of the logits where the best expert
-        // ranks the group); lane g keeps group g's score
-        auto group_key = [&](int i) {
-            return top2 && !a.bias && key[i] > order_key(-INFINITY) ? order_key(s[i]) : key[i];
-        };
-        auto merge = [](uint32_t& a1, uint32_t& a2, uint32_t b1, uint32_t b2) {
-            a2 = max(min(a1, b1), max(a2, b2));
-            a1 = max(a1, b1);
-        };
-        auto score = [&](uint32_t a1, uint32_t a2) {
-            const float best = a1 ? key_value(a1) : -INFINITY;
-            return top2 && a2 > order_key(-INFINITY) ? best + key_value(a2) : best;
-        };
-        const int lanes = plan.lanes;
-        float my = -INFINITY;
-        if (lanes) {
-            uint32_t a1 = 0u, a2 = 0u;
+    // A group's score from the two largest keys of c (of the logits without a bias, whose order is that of
+    // s; where the best expert ranks the group, they are its score).
+    constexpr uint32_t MASKED = 0x007fffffu;  // order_key(-INFINITY)
+    auto score = [&](uint32_t a1, uint32_t a2) {
+        const float best = a1 ? key_value(a1) : -INFINITY;
+        if (!top2) return best;
+        auto part = [&](float x) { return a.bias ? x : approx(x) * inv; };
+        return a1 <= MASKED ? -INFINITY : a2 <= MASKED ? part(best) : part(best) + part(key_value(a2));
+    };
+    auto merge = [](uint32_t& a1, uint32_t& a2, uint32_t b1, uint32_t b2) {
+        a2 = max(min(a1, b1), max(a2, b2));
+        a1 = max(a1, b1);
+    };
+    uint32_t* keys = reinterpret_cast<uint32_t*>(c64);  // [32][EPL]
+    auto store_keys = [&] {
+        __syncwarp();
+        if (EPL % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) merge(a1, a2, group_key(i), 0u);
-            for (int off = 1; off < lanes; off <<= 1) {
-                const uint32_t b1 = __shfl_xor_sync(0xffffffffu, a1, off), b2 = __shfl_xor_sync(0xffffffffu, a2, off);
-                merge(a1, a2, b1, b2);
-            }
-            my = __shfl_sync(0xffffffffu, score(a1, a2), min(lane * lanes, 31));
+            for (int i = 0; i + 3 < EPL; i += 4)
+                reinterpret_cast<uint4*>(keys + lane * EPL)[i / 4] = make_uint4(key[i], key[i + 1], key[i + 2], key[i + 3]);
         } else {
-            for (int g = 0; g < a.n_group; ++g) {
-                uint32_t a1 = 0u, a2 = 0u;
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) {
-                    const int e = lane * EPL + i - g * gs;
-                    if (e >= 0 && e < gs) merge(a1, a2, group_key(i), 0u);
-                }
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) {
-                    const uint32_t b1 = __shfl_xor_sync(0xffffffffu, a1, off), b2 = __shfl_xor_sync(0xffffffffu, a2, off);
-                    merge(a1, a2, b1, b2);
-                }
-                if (lane == g) my = score(a1, a2);
-            }
+            for (int i = 0; i < EPL; ++i) keys[lane * EPL + i] = key[i];
         }
+        __syncwarp();
+    };
+    if (GROUPS) {
+        // each group's two largest keys from its lanes, or where a group has no lanes of its own out of
+        // shared memory by `lanes` others, then lane g has group g's (16384 tokens x 160 experts in 8 groups:
+        // 33 us; each group by the whole warp from the registers 53)
+        const int gs = plan.gs;
+        int lanes = plan.lanes;
+        uint32_t a1 = 0u, a2 = 0u;
+        if (lanes) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) merge(a1, a2, key[i], 0u);
+        } else {
+            lanes = 1 << (31 - __clz(32 / a.n_group));
+            const int g = lane / lanes;
+            store_keys();
+            if (g < a.n_group)
+                for (int e = g * gs + lane % lanes; e < (g + 1) * gs; e += lanes) merge(a1, a2, keys[e], 0u);
+        }
+        for (int off = 1; off < lanes; off <<= 1) {
+            const uint32_t b1 = __shfl_xor_sync(0xffffffffu, a1, off), b2 = __shfl_xor_sync(0xffffffffu, a2, off);
+            merge(a1, a2, b1, b2);
+        }
+        const float my = __shfl_sync(0xffffffffu, score(a1, a2), min(lane * lanes, 31));
         int rank = 0;  // how many groups come before this lane's
         for (int h = 0; h < a.n_group; ++h) {
             const float o = __shfl_sync(0xffffffffu, my, h);
@@ -404,7 +415,7 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
             const float slack = (softmax ? 0x1p-17f * 2.0f + 0x1p-19f : 0x1p-20f * 4.0f) + 0x1p-22f * 4.0f * (1.0f + bmax);
             if (!(lo - hi > slack)) keep = groups64<BF16>(a, t, mx, c64);
         }
-        if (lanes) {
+        if (plan.lanes) {
             const int g = lane >> plan.shift;
             if (g < a.n_group && !(keep >> g & 1u)) {
 #pragma unroll
@@ -416,60 +427,54 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
                 if (i < live && !(keep >> ((lane * EPL + i) / gs) & 1u)) key[i] = 0u;
         }
     }
-    // Top-k: every lane sorts its keys, and the warp takes the largest of the lanes' heads, the lowest
-    // lane's among equal ones. Which of the lane's experts a key is, is looked up afterwards from the
-    // unsorted keys in shared memory; of a lane's equal keys the n-th taken is the n-th in order of id.
-    // With a bias the candidates go on to those within the error of the last chosen, and where two
-    // neighbours are that close, fp64 orders the candidates: any other expert is below topk of them.
-    uint32_t* keys = reinterpret_cast<uint32_t*>(c64);  // [32][EPL]
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) keys[lane * EPL + i] = key[i];
+    // Every lane sorts its keys. Which of its experts a key is, is looked up afterwards from the unsorted
+    // keys in shared memory; of a lane's equal keys the n-th taken is the n-th in order of id.
+    store_keys();
     sort_keys<EPL>(key);
-    uint32_t taken = 0u, my_key = 0u;  // the lane's last key taken; the key of candidate `lane`
-    int equals = 0, my_equals = 0, my_from = 0, count = 0;
-    // the slack of two c: s_i + s_j <= |c_i| + |c_j| + 2 bmax for softmax; sigmoid's s are at most 1
+    // Top-k: the warp takes the largest of the lanes' heads, the lowest lane's among equal ones, topk
+    // times (the kept groups hold as many experts); lane j keeps the j-th. With a bias the candidates go
+    // on to those within the error of the last chosen, and where two neighbours are that close, fp64
+    // orders the candidates: any other expert is below topk of them.
+    // The slack of two c: s_i + s_j <= |c_i| + |c_j| + 2 bmax for softmax; sigmoid's s are at most 1.
     const float slack0 = softmax ? 0x1p-16f * bmax + 0x1p-20f * inv : 0x1p-19f + 0x1p-21f * (1.0f + bmax);
     const float slack1 = softmax ? 0x1p-17f + 0x1p-22f : 0.0f;
-    float prev = INFINITY, last = INFINITY;
-    bool close = false;
-    for (int j = 0;; ++j) {
-        if (j >= a.topk && !a.bias) break;
+    // masked experts (c = -inf, no slack) are behind every live one, in order of id
+    auto near = [&](float hi, float c) {
+        return c > -INFINITY && !(hi - c > slack0 + slack1 * (fabsf(hi) + fabsf(c)));
+    };
+    uint32_t my_key = 0u, last = 0u;
+    int my_from = 0, count = 0;
+    for (;; ++count) {
         const uint32_t top = __reduce_max_sync(0xffffffffu, key[0]);
-        if (top == 0u) break;  // none left; the kept groups hold at least topk experts
-        if (a.bias) {
-            const float c = key_value(top);
-            // masked experts (c = -inf, no slack) are behind every live one, in order of id
-            auto near = [&](float hi) { return c > -INFINITY && !(hi - c > slack0 + slack1 * (fabsf(hi) + fabsf(c))); };
-            if (j >= a.topk && !near(last)) break;
-            if (j && near(prev)) close = true;
-            prev = c;
-            if (j < a.topk) last = c;
-        }
-        if (j == 32) return false;
+        if (count < a.topk) last = top;
+        else if (!a.bias || top == 0u || !near(key_value(last), key_value(top))) break;
+        if (count == 32) return false;
         const int from = __ffs(__ballot_sync(0xffffffffu, key[0] == top)) - 1;
-        const int same = taken == top ? equals + 1 : 0;  // of the lane that is taken from
-        const int theirs = __shfl_sync(0xffffffffu, same, from);
-        if (lane == j) {
+        if (lane == count) {
             my_key = top;
             my_from = from;
-            my_equals = theirs;
         }
         if (lane == from) {
-            taken = top;
-            equals = same;
 #pragma unroll
             for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
             key[EPL - 1] = 0u;
         }
-        count = j + 1;
     }
-    __syncwarp();
+    bool close = false;
+    if (a.bias) {
+        const float c = key_value(my_key), before = __shfl_up_sync(0xffffffffu, c, 1);
+        close = __any_sync(0xffffffffu, lane > 0 && lane < count && near(before, c));
+    }
+    // a lane's equal keys are taken one after the other: lane j's is the n-th of its like
+    const uint32_t key_before = __shfl_up_sync(0xffffffffu, my_key, 1);
+    const int from_before = __shfl_up_sync(0xffffffffu, my_from, 1);
+    const uint32_t firsts = __ballot_sync(0xffffffffu, lane == 0 || key_before != my_key || from_before != my_from);
+    int n = __clz(firsts << (31 - lane));
     int my_id = 0;
     if (lane < count) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (keys[my_from * EPL + i] == my_key && my_equals-- == 0) my_id = my_from * EPL + i;
+            if (keys[my_from * EPL + i] == my_key && n-- == 0) my_id = my_from * EPL + i;
     }
     if (close) my_id = order64<BF16>(a, t, mx, my_id, count);
     const bool mine = lane < a.topk;
@@ -525,13 +530,13 @@ MOE_DEV void load_logits(const moe_route_args_t& a, const void* row, bool wide, 
         for (int i = 0; i < EPL; ++i) l[i] = e0 + i < a.E ? load_logit<BF16>(row, e0 + i) : -INFINITY;
     }
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-        if (isnan(l[i])) l[i] = -INFINITY;
+    for (int i = 0; i < EPL; ++i) l[i] = fmaxf(l[i], -INFINITY);
 }
 
 template <int EPL, bool BF16, bool GROUPS>
-__global__ void __launch_bounds__(128) route_scored_kernel(const moe_route_args_t a, const RoutePlan plan) {
-    extern __shared__ double warps_c64[];  // [warps]: 32 EPL keys, or E values of a token taken up in fp64
+__global__ void __launch_bounds__(128, EPL <= 8 ? 8 : 4) route_scored_kernel(const moe_route_args_t a, const RoutePlan plan) {
+    // [warps]: 32 EPL keys, or E values of a token taken up in fp64
+    extern __shared__ __align__(16) double warps_c64[];
     pdl_wait();
     const int t = blockIdx.x * (blockDim.x >> 5) + warp_id();
     if (t < a.T) {
@@ -548,7 +553,6 @@ template <int EPL, bool BF16>
 cudaError_t run_route(const moe_route_args_t& r, cudaStream_t st, bool pdl) {
     const dim3 grid((r.T - 1) / 4 + 1), block(128);
     const int bytes = BF16 ? 2 : 4;
-    const size_t smem = 4 * sizeof(double) * 32 * EPL;  // at most 32 KB
     RoutePlan p{};
     p.wide = (reinterpret_cast<uintptr_t>(r.logits) & 15) == 0 && r.row_stride * bytes % 16 == 0 && r.E * bytes % 16 == 0;
     p.wide_bias = (reinterpret_cast<uintptr_t>(r.bias) & 15) == 0 && r.E == 32 * EPL;
@@ -557,6 +561,7 @@ cudaError_t run_route(const moe_route_args_t& r, cudaStream_t st, bool pdl) {
         p.lanes = p.gs / EPL;
         while ((1 << p.shift) < p.lanes) ++p.shift;
     }
+    const size_t smem = 4 * sizeof(double) * 32 * EPL;  // at most 32 KB
     if (r.topk_group < r.n_group) return launch_k(route_scored_kernel<EPL, BF16, true>, grid, block, smem, st, pdl, r, p);
     return launch_k(route_scored_kernel<EPL, BF16, false>, grid, block, smem, st, pdl, r, p);
 }
