@@ -432,13 +432,17 @@ moe_status_t moe_quantize_mxfp4(const void* in, int in_is_f32, int64_t in_stride
  *   w       MXFP4 weights prepared by moe_prepare_weights (else NOT_PREPARED); other formats:
  *           UNSUPPORTED.
  *   out bf16 [M_alloc, N], N % 8 == 0; cu_seqlens int32 [G] on device; G <= 1024.
+ *   rows: with row_idx, room for moe_grouped_gemm_mxfp4_rows_size bytes (16-byte aligned), into which
+ *           long segments are gathered before their product, or NULL: the product gathers them as it
+ *           goes, slower for such segments. The size is 0 where the room would not be used.
  *   ws: at least 256 bytes (the error word). The first call on a device sets kernel attributes:
  *   make it before any stream capture.
  */
 moe_status_t moe_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int a_rows,
                                     const int32_t* row_idx, int M_alloc, const moe_weight_t* w,
-                                    const int32_t* cu_seqlens, void* out, void* ws, size_t ws_bytes,
+                                    const int32_t* cu_seqlens, void* out, void* rows, void* ws, size_t ws_bytes,
                                     moe_stream_t stream);
+size_t moe_grouped_gemm_mxfp4_rows_size(int M_alloc, const moe_weight_t* w);
 
 /*
  * S0 — one-time conversion of FP4 weights into the kernel's tile layout

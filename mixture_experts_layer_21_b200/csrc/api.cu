@@ -268,9 +268,14 @@ moe_status_t moe_quantize_mxfp4(const void* in, int in_is_f32, int64_t in_stride
     return cuda_status(launch_quant_mxfp4(in, in_is_f32 != 0, in_stride, R, K, codes, scales, deq, S(stream), false));
 }
 
+size_t moe_grouped_gemm_mxfp4_rows_size(int M_alloc, const moe_weight_t* w) {
+    if (!w || M_alloc < 1 || w->G < 1 || w->N < 1 || w->K < 1) return 0;
+    return gemm_mxf4_rows_bytes(w->G, w->N, w->K, M_alloc);
+}
+
 moe_status_t moe_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int a_rows, const int32_t* row_idx,
-                                    int M_alloc, const moe_weight_t* w, const int32_t* cu_seqlens, void* out, void* ws,
-                                    size_t ws_bytes, moe_stream_t stream) {
+                                    int M_alloc, const moe_weight_t* w, const int32_t* cu_seqlens, void* out, void* rows,
+                                    void* ws, size_t ws_bytes, moe_stream_t stream) {
     if (!w || M_alloc < 0 || a_rows < 0 || w->G < 1 || w->N < 1 || w->K < 1) return MOE_ERR_INVALID_ARG;
     if (w->G > 1024) return MOE_ERR_UNSUPPORTED;
     if (w->fmt != MOE_W_MXFP4) return MOE_ERR_UNSUPPORTED;
@@ -279,10 +284,11 @@ moe_status_t moe_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_sca
     if (M_alloc == 0) return MOE_OK;
     if (a_rows < 1 || (!row_idx && a_rows < M_alloc)) return MOE_ERR_INVALID_ARG;
     if (!a_codes || !a_scales || !cu_seqlens || !out || !ws) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(a_codes) || !aligned16(out) || w->N % 8) return MOE_ERR_ALIGNMENT;
+    if (!aligned16(a_codes) || !aligned16(out) || !aligned16(rows) || w->N % 8) return MOE_ERR_ALIGNMENT;
     if (ws_bytes < kErrBytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
     const Mxf4Problem p{a_codes,   a_scales,  a_rows,          row_idx,    M_alloc, w->G, w->N, w->K,
-                        w->kdata,  w->kscale, weight_alpha(*w), cu_seqlens, out,     reinterpret_cast<DevError*>(ws)};
+                        w->kdata,  w->kscale, weight_alpha(*w), cu_seqlens, out,     reinterpret_cast<DevError*>(ws),
+                        rows};
     return cuda_status(launch_gemm_mxf4(p, S(stream), false));
 }
 

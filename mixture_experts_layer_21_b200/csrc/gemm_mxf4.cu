@@ -17,7 +17,8 @@
 //
 // PAIR: two SMs per tile (a cluster of two CTAs, cta_group::2). A pair tile is 256 weight rows, 128
 // from each CTA's shared memory, by up to BT tokens, half of them from each, so an SM moves half the
-// token operand per product. The leader (rank 0) issues MMAs and scale copies for both.
+// token operand per product. The leader (rank 0) issues MMAs and scale copies for both. Pairs take token
+// rows in segment order only; a kernel of its own brings them into it first.
 //
 // The scales run ahead of the codes in a ring of their own, so that their way through registers,
 // shared and tensor memory is not in line with the codes' copies. Warp roles, each run by whole warps
@@ -30,7 +31,7 @@
 //   gather     four warps, likewise (with row_idx): the token rows' codes by cp.async
 // Barriers, all with bounded waits as in the other GEMMs (s stage, d scale-ring entry, t slot, b buffer):
 //   full[s]      the TMA copies of stage s landed (PAIR: on the leader, both CTAs' copies)
-//   gfull[s]     this CTA's gathered rows of stage s landed; pfull[s], on the leader: the peer's
+//   gfull[s]     the gathered rows of stage s landed
 //   empty[s]     the MMAs that read stage s completed (both CTAs)
 //   sf_ready[d]  this CTA's scale blocks are in the ring; psf[d], on the leader: the peer's
 //   sf_free[d]   they were copied (both CTAs)
@@ -112,7 +113,7 @@ struct Mxf4Cfg {
     static constexpr int GATHER_WARP0 = SCALE_WARP0 + kScaleWarps;
     static constexpr int THREADS = (GATHER_WARP0 + (GATHER ? kGatherWarps : 0)) * 32;
     static_assert(BT % 16 == 0 && BT >= 16 && BT <= 240, "token tile");
-    static_assert(!PAIR || BT % 32 == 0, "pair MMA N: a multiple of 32");
+    static_assert(!PAIR || (BT % 32 == 0 && !GATHER), "pair MMA N: a multiple of 32; tokens by TMA");
     static_assert(STAGES >= 3 && SLOTS >= 2 && SMEM_BYTES <= kSmemLimit && SF_BASE + SLOTS * SF_SLOT <= 512, "MXFP4 GEMM config");
     static_assert(B_BYTES % 1024 == 0, "operand alignment");
     // a warp that takes every n-th turn of a ring finds the turn of an entry before its own finished
@@ -164,7 +165,6 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
     auto opB = [&](int s) { return smem + s * C::STAGE + C::A_BYTES; };
     auto sfA = [&](int d) { return sf_ring + d * C::SF_ENTRY; };
     auto sfB = [&](int d, int h, int rg) { return sf_ring + d * C::SF_ENTRY + 1024 + (h * C::RG + rg) * 512; };
-    uint64_t* pfull = ctl->raw_full;
     const int warp = __shfl_sync(0xffffffffu, warp_id(), 0), lane = lane_id();
     const int G = a.G, NT = a.NT, KB = a.KB;  // NT: blocks of 128 weight rows, or of 256 (PAIR)
     const int rank = PAIR ? (int)cluster_ctarank() : 0;
@@ -193,7 +193,6 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             mbar_init(&ctl->full[s], 1);
             mbar_init(&ctl->empty[s], 1);
             mbar_init(&mc->gfull[s], 32);  // the lanes of the gather warp that copied the stage's rows
-            mbar_init(&pfull[s], 1);
         }
         for (int d = 0; d < kSfRing; ++d) {
             mbar_init(&mc->sf_ready[d], 2);  // the weights' copy and the tokens' scale warp
@@ -301,8 +300,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                 const uint32_t d = tmem_base + (uint32_t)(b * BT);
                 for (int kb = 0; kb < KB; ++kb) {
                     if ((!next_sf && !wait(&mc->sf_full[sl.i], sl.ph)) || (!next_full && !wait(&ctl->full[st.i], st.ph)) ||
-                        (!next_g && !wait(&mc->gfull[st.i], st.ph)) ||
-                        (GATHER && PAIR && !wait(&pfull[st.i], st.ph))) {
+                        (!next_g && !wait(&mc->gfull[st.i], st.ph))) {
                         ok = false;
                         break;
                     }
@@ -346,23 +344,6 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                 if (b == 0) bph ^= 1u;
             }
             if (!ok) give_up(2);
-        } else if (GATHER) {
-            // peer: tells the leader that its gathered rows of each stage landed
-            Ring st;
-            bool ok = true;
-            for (int L = first_tile; L < total && ok; L += tile_step) {
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!wait(&mc->gfull[st.i], st.ph)) {
-                        ok = false;
-                        break;
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (elect_one()) mbar_arrive_remote(mapa_shared(smem_u32(&pfull[st.i]), 0));
-                    st.next(C::STAGES);
-                }
-            }
-            if (!ok) give_up(6);
         }
     } else if (warp == C::COPIER_WARP) {
         // ---------------- scale blocks: ring -> tensor memory (peer: tells the leader they are in its ring)
@@ -556,14 +537,14 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
         for (int L = first_tile; L < total && ok; L += tile_step) {
             int g, nt, row0, rows;
             tile(L, g, nt, row0, rows);
-            const int p0 = part0(rows), part = PAIR ? mma_n(rows) / 2 : mma_n(rows);  // 16 rows at least
+            const int part = mma_n(rows);
             __syncwarp();
             for (int i = lane; i < part; i += 32) {
                 int v = -1;
-                if (p0 + i < rows) {
-                    v = a.row_idx[row0 + p0 + i];
+                if (i < rows) {
+                    v = a.row_idx[row0 + i];
                     if (v < 0 || v >= a.a_rows) {  // counts as a row of zeros
-                        report_error(a.err, MOE_ERR_DEVICE, row0 + p0 + i);
+                        report_error(a.err, MOE_ERR_DEVICE, row0 + i);
                         v = -1;
                     }
                 }
@@ -592,7 +573,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             }
         }
         cp_async_wait_all();
-        if (!ok) give_up(7);
+        if (!ok) give_up(6);
     }
 
     // After an abort (PAIR: always; in a normal run these waits return at once) every role lets what
@@ -674,12 +655,85 @@ cudaError_t run_mxf4_bt(const Mxf4Problem& p, const CUtensorMap& tw, const Mxf4A
     if (!make_map_u8(&ta, p.a_codes, (uint64_t)p.K / 2, p.a_rows, p.K / 2, kStageK / 2, PAIR ? BT / 2 : BT,
                      CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    return p.row_idx ? run_mxf4<BT, true, PAIR>(ta, tw, a, st, pdl) : run_mxf4<BT, false, PAIR>(ta, tw, a, st, pdl);
+    return p.row_idx ? run_mxf4<BT, !PAIR, PAIR>(ta, tw, a, st, pdl) : run_mxf4<BT, false, PAIR>(ta, tw, a, st, pdl);
+}
+
+// The rows that row_idx names, copied into segment order, a warp to a row: where the product runs on CTA
+// pairs a row's codes are read once for every 256 weight rows, and the product of rows in order is faster
+// by more than the copy takes (8192 rows x 4096 into 14336: 246 us against 289, the copy 6). Rows behind
+// the segments are left out: their row_idx may be anything.
+__global__ void __launch_bounds__(256) gather_mxfp4_rows_kernel(const uint8_t* __restrict__ codes,
+                                                                const uint8_t* __restrict__ scales, int a_rows,
+                                                                const int32_t* __restrict__ row_idx,
+                                                                const int32_t* __restrict__ cu, int G, int M, int K,
+                                                                uint8_t* codes_out, uint8_t* scales_out, DevError* err) {
+    pdl_wait();
+    const int lane = lane_id();
+    const long long r = (long long)blockIdx.x * 8 + warp_id();
+    int end = 0;
+    for (int g = lane; g < G; g += 32) end = max(end, cu[g]);
+    end = min(__reduce_max_sync(0xffffffffu, end), M);
+    if (r < end) {
+        const int v = row_idx[r];
+        const bool ok = v >= 0 && v < a_rows;
+        if (!ok && lane == 0) report_error(err, MOE_ERR_DEVICE, (int)r);  // counts as a row of zeros
+        const int nc = K / 32;  // 16 codes bytes and one scale byte per 32 values
+        const uint4* s = reinterpret_cast<const uint4*>(codes) + (size_t)(ok ? v : 0) * nc;
+        uint4* d = reinterpret_cast<uint4*>(codes_out) + (size_t)r * nc;
+        const uint8_t* ss = scales + (size_t)(ok ? v : 0) * nc;
+        uint8_t* ds = scales_out + (size_t)r * nc;
+#pragma unroll 4
+        for (int i = lane; i < nc; i += 32) {
+            d[i] = ok ? __ldg(s + i) : make_uint4(0u, 0u, 0u, 0u);
+            ds[i] = ok ? __ldg(ss + i) : (uint8_t)0;
+        }
+    }
+    pdl_launch();
+}
+
+// Token tile: a tile costs a stage per 256 K whatever its width, so it should hold a whole segment;
+// mean + 2 sqrt(mean) covers nearly every one. Longer segments go to CTA pairs, where there is a
+// tile for each pair of SMs: 8 experts x 14336 x 4096 with 128 rows each took 56 us on pairs, 59 in
+// 128-token tiles, with 1024 rows 246 and 295; with 64 rows 53 and 49.
+// MOE_TOKEN_TILE=16|32|64|128 and MOE_GEMM_PAIRS=0|1 override the choice (tests, tuning).
+// Returns 16, 32, 64 or 128, or, where rows are in segment order or can be brought into it, kPairTile.
+constexpr int kPairTile = 192;
+int mxf4_tile(int G, int N, int M_alloc, bool pairs) {
+    const long long segs = std::max<long long>(1, std::min<long long>(G, M_alloc));
+    const double avg = (double)M_alloc / (double)segs;
+    const char* env = getenv("MOE_TOKEN_TILE");
+    const int v = env ? atoi(env) : 0;
+    const bool forced = v == 16 || v == 32 || v == 64 || v == 128;
+    const double want = forced ? v : avg + 2.0 * std::sqrt(avg);
+    const char* pe = getenv("MOE_GEMM_PAIRS");
+    const int mode = pe && (pe[0] == '0' || pe[0] == '1') && pe[1] == '\0' ? pe[0] - '0' : 2;
+    const int nt1 = (N + kTileN - 1) / kTileN;
+    const long long pair_tiles = ((long long)M_alloc + kPairTile - 1) / kPairTile * ((nt1 + 1) / 2);
+    if (pairs && (mode == 1 || (mode == 2 && want > 128 && pair_tiles >= num_sms() / 2))) return kPairTile;
+    return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
 }
 
 }  // namespace
 
-cudaError_t launch_gemm_mxf4(const Mxf4Problem& p, cudaStream_t st, bool pdl) {
+size_t gemm_mxf4_rows_bytes(int G, int N, int K, int M_alloc) {
+    return mxf4_tile(G, N, M_alloc, true) == kPairTile ? (size_t)M_alloc * (K / 2 + K / 32) : 0;
+}
+
+cudaError_t launch_gemm_mxf4(const Mxf4Problem& problem, cudaStream_t st, bool pdl) {
+    Mxf4Problem p = problem;
+    const int bt = mxf4_tile(p.G, p.N, p.M_alloc, !p.row_idx || p.rows);
+    if (bt == kPairTile && p.row_idx) {
+        uint8_t* codes = static_cast<uint8_t*>(p.rows);
+        uint8_t* scales = codes + (size_t)p.M_alloc * (p.K / 2);
+        const cudaError_t e = launch_k(gather_mxfp4_rows_kernel, dim3((p.M_alloc - 1) / 8 + 1), dim3(256), 0, st, pdl, p.a_codes,
+                                       p.a_scales, p.a_rows, p.row_idx, p.cu_seqlens, p.G, p.M_alloc, p.K, codes, scales, p.err);
+        if (e != cudaSuccess) return e;
+        p.a_codes = codes;
+        p.a_scales = scales;
+        p.a_rows = p.M_alloc;
+        p.row_idx = nullptr;
+        pdl = true;
+    }
     const int Kp = mx8_kpad(p.K);
     Mxf4Args a{};
     a.cu = p.cu_seqlens;
@@ -702,25 +756,10 @@ cudaError_t launch_gemm_mxf4(const Mxf4Problem& p, cudaStream_t st, bool pdl) {
     l2_policies(&a.l2_w, &a.l2_t);
     CUtensorMap tw;
     if (!make_map_codes(&tw, p.kdata, (uint64_t)Kp / 2, p.N, p.G)) return cudaErrorInvalidValue;
-    // Token tile: a tile costs a stage per 256 K whatever its width, so it should hold a whole segment;
-    // mean + 2 sqrt(mean) covers nearly every one. Longer segments go to CTA pairs, where there is a
-    // tile for each pair of SMs: 8 experts x 14336 x 4096 with 128 rows each took 56 us on pairs, 59 in
-    // 128-token tiles (62 and 73 gathered), with 1024 rows 246 and 295; with 64 rows 53 and 49.
-    // MOE_TOKEN_TILE=16|32|64|128 and MOE_GEMM_PAIRS=0|1 override the choice (tests, tuning).
-    const long long segs = std::max<long long>(1, std::min<long long>(p.G, p.M_alloc));
-    const double avg = (double)p.M_alloc / (double)segs;
-    const char* env = getenv("MOE_TOKEN_TILE");
-    const int v = env ? atoi(env) : 0;
-    const bool forced = v == 16 || v == 32 || v == 64 || v == 128;
-    const double want = forced ? v : avg + 2.0 * std::sqrt(avg);
-    const char* pe = getenv("MOE_GEMM_PAIRS");
-    const int mode = pe && (pe[0] == '0' || pe[0] == '1') && pe[1] == '\0' ? pe[0] - '0' : 2;
-    const long long pair_tiles = ((long long)p.M_alloc + 191) / 192 * ((a.NT1 + 1) / 2);
-    if (mode == 1 || (mode == 2 && want > 128 && pair_tiles >= num_sms() / 2))
-        return run_mxf4_bt<192, true>(p, tw, a, st, pdl);
-    if (want <= 16) return run_mxf4_bt<16>(p, tw, a, st, pdl);
-    if (want <= 32) return run_mxf4_bt<32>(p, tw, a, st, pdl);
-    if (want <= 64) return run_mxf4_bt<64>(p, tw, a, st, pdl);
+    if (bt == kPairTile) return run_mxf4_bt<kPairTile, true>(p, tw, a, st, pdl);
+    if (bt == 16) return run_mxf4_bt<16>(p, tw, a, st, pdl);
+    if (bt == 32) return run_mxf4_bt<32>(p, tw, a, st, pdl);
+    if (bt == 64) return run_mxf4_bt<64>(p, tw, a, st, pdl);
     return run_mxf4_bt<128>(p, tw, a, st, pdl);
 }
 

@@ -188,7 +188,9 @@ struct Mxf4Problem {
     const int32_t* cu_seqlens;
     void* out;
     DevError* err;
+    void* rows;  // room for the gathered rows (gemm_mxf4_rows_bytes), or null
 };
+size_t gemm_mxf4_rows_bytes(int G, int N, int K, int M_alloc);
 cudaError_t launch_gemm_mxf4(const Mxf4Problem& p, cudaStream_t st, bool pdl);
 int choose_token_tile(long long NvS, int G, bool wide_ok);
 

@@ -38,10 +38,11 @@ def test_quantize_refuses(kw, want):
 
 
 def _gemm(w=None, **kw):
-    d = dict(a=16, s=1, rows=8, idx=None, M=8, cu=16, out=16, ws=16, nws=256)
+    d = dict(a=16, s=1, rows=8, idx=None, M=8, cu=16, out=16, room=None, ws=16, nws=256)
     d.update(kw)
     return L.moe_grouped_gemm_mxfp4(d["a"], d["s"], d["rows"], d["idx"], d["M"],
-                                    None if w is None else ctypes.byref(w), d["cu"], d["out"], d["ws"], d["nws"], None)
+                                    None if w is None else ctypes.byref(w), d["cu"], d["out"], d["room"], d["ws"], d["nws"],
+                                    None)
 
 
 def _w(fmt=1, G=2, N=64, K=64, prepared=True):
@@ -55,7 +56,7 @@ def _w(fmt=1, G=2, N=64, K=64, prepared=True):
     (None, {}, INVALID), (_w(), dict(M=-1), INVALID), (_w(), dict(rows=-1), INVALID), (_w(), dict(rows=7), INVALID),
     (_w(), dict(rows=0, idx=16), INVALID), (_w(G=0), {}, INVALID), (_w(N=0), {}, INVALID), (_w(K=0), {}, INVALID),
     (_w(G=1025), {}, UNSUP), (_w(fmt=0), {}, UNSUP), (_w(fmt=2), {}, UNSUP), (_w(prepared=False), {}, NOT_PREP),
-    (_w(K=48), {}, ALIGN), (_w(N=60), {}, ALIGN), (_w(), dict(a=8), ALIGN), (_w(), dict(out=8), ALIGN),
+    (_w(K=48), {}, ALIGN), (_w(N=60), {}, ALIGN), (_w(), dict(a=8), ALIGN), (_w(), dict(out=8), ALIGN), (_w(), dict(room=8), ALIGN),
     (_w(), dict(a=None), INVALID), (_w(), dict(s=None), INVALID), (_w(), dict(cu=None), INVALID),
     (_w(), dict(out=None), INVALID), (_w(), dict(ws=None), INVALID), (_w(), dict(nws=255), WS_SMALL),
     (_w(), dict(M=0, a=None, cu=None), 0)])
@@ -352,6 +353,95 @@ def test_product_graph_on_two_streams():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], _product(second[:2] + cases[0][2:4] + second[4:])[0])
+
+
+def test_room_for_gathered_rows(monkeypatch):
+    size = lambda M, w: L.moe_grouped_gemm_mxfp4_rows_size(M, None if w is None else ctypes.byref(w))
+    monkeypatch.setenv("MOE_GEMM_PAIRS", "1")
+    assert size(7, _w(K=96)) == 7 * (48 + 3)
+    assert size(2 ** 31 - 1, _w(K=4096)) == (2 ** 31 - 1) * 2176
+    assert size(0, _w()) == size(-1, _w()) == size(7, None) == size(7, _w(K=0)) == 0
+    monkeypatch.setenv("MOE_GEMM_PAIRS", "0")
+    assert size(7, _w(K=96)) == 0
+    monkeypatch.delenv("MOE_GEMM_PAIRS")
+    assert size(7, _w(G=2, N=64)) == 0                # few rows: gathered by the product
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,N,K", [([3, 0, 200, 1, 391], 136, 32), ([130, 70], 264, 7200), ([5] * 77 + [0] * 9, 72, 480)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_product_rows_gathered_first(lens, N, K, shift, monkeypatch):
+    """The gather before the CTA pairs: bad indices in the segments, arbitrary ones behind them, scales at
+    an odd address, more segments than a warp has lanes."""
+    monkeypatch.setenv("MOE_GEMM_PAIRS", "1")
+    case = list(_case(lens, N, K, True, seed=K, T=50, pad=9))
+    M, idx = case[-1], case[4]
+    idx[M - 9:] = torch.tensor([-1, 50, 2 ** 31 - 1, -2 ** 31, 0, 49, 7, -5, 1000])
+    _check_product(case)
+    idx[0], idx[2], idx[M - 10] = -1, 50, 2 ** 31 - 1
+    ac, asc, wc, wsc, idx, al, cu, M = case
+    w = m.moe_prepare_weights(m.Weight("mxfp4", wc.cuda(), wsc.cuda()))
+    sc = torch.zeros(asc.numel() + 8, dtype=torch.uint8, device="cuda")[shift:shift + asc.numel()].view(asc.shape)
+    sc.copy_(asc)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    got = m.moe_grouped_gemm_mxfp4(ac.cuda(), sc, w, cu.cuda(), idx.cuda(), ws=ws)
+    torch.cuda.synchronize()
+    assert m.moe_get_device_error(ws) == DEVICE
+    ref, slack = _reference(case)
+    assert np.all(np.abs(got.double().cpu().numpy() - ref) <= slack + (np.abs(ref) + slack) * 2.0 ** -8)
+
+
+@pytest.mark.gpu
+def test_product_without_room_gathers_as_it_goes(monkeypatch):
+    monkeypatch.setenv("MOE_GEMM_PAIRS", "1")
+    case = _case([150, 0, 260], 264, 352, True, seed=13, T=90, pad=4)
+    ac, asc, wc, wsc, idx, al, cu, M = [t.cuda() if torch.is_tensor(t) else t for t in case]
+    w = m.moe_prepare_weights(m.Weight("mxfp4", wc, wsc))
+    out = torch.empty(M, 264, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    st = L.moe_grouped_gemm_mxfp4(ac.data_ptr(), asc.data_ptr(), 90, idx.data_ptr(), M, ctypes.byref(w.desc), cu.data_ptr(),
+                                  out.data_ptr(), None, ws.data_ptr(), 256, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    ref, slack = _reference(case)
+    assert st == 0 and m.moe_get_device_error(ws) == 0
+    assert np.all(np.abs(out.double().cpu().numpy() - ref) <= slack + (np.abs(ref) + slack) * 2.0 ** -8)
+
+
+@pytest.mark.gpu
+def test_product_rows_gathered_first_on_streams_and_in_graphs(monkeypatch):
+    """The room belongs to the call: two streams at once, its memory reused on the current stream meanwhile,
+    and two captured graphs replayed on new indices."""
+    monkeypatch.setenv("MOE_GEMM_PAIRS", "1")
+    cases = [_case([400, 60, 0, 333], 512, 2048, True, seed=s, T=300) for s in (1, 2)]
+    dev = [[None if t is None else t.cuda() for t in c[:7]] for c in cases]
+    ws = [m.moe_prepare_weights(m.Weight("mxfp4", d[2], d[3])) for d in dev]
+    outs = [torch.empty(793, 512, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    err = [torch.zeros(256, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    want = [_product(c)[0] for c in cases]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    call = lambda i, st=None: m.moe_grouped_gemm_mxfp4(dev[i][0], dev[i][1], ws[i], dev[i][6], dev[i][4], outs[i], err[i], st)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            call(i, st)
+            torch.full((793 * 1088,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, g in enumerate(graphs):
+        with torch.cuda.graph(g):
+            call(i)
+    second = [_case([400, 60, 0, 333], 512, 2048, True, seed=s, T=300) for s in (5, 6)]
+    for i in range(2):
+        dev[i][4].copy_(second[i][4])
+    for st, g in zip(streams, graphs):
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            for _ in range(5):
+                g.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(outs[i], _product(cases[i][:4] + second[i][4:5] + cases[i][5:])[0])
 
 
 @pytest.mark.gpu
