@@ -433,8 +433,8 @@ moe_status_t moe_quantize_mxfp4(const void* in, int in_is_f32, int64_t in_stride
  *           UNSUPPORTED.
  *   out bf16 [M_alloc, N], N % 8 == 0; cu_seqlens int32 [G] on device; G <= 1024.
  *   rows: with row_idx, room for moe_grouped_gemm_mxfp4_rows_size bytes (16-byte aligned), into which
- *           long segments are gathered before their product, or NULL: the product gathers them as it
- *           goes, slower for such segments. The size is 0 where the room would not be used.
+ *           segments of many rows are gathered before their product, or NULL: the product gathers
+ *           them as it goes, slower for such segments. The size is 0 where it is not used.
  *   ws: at least 256 bytes (the error word). The first call on a device sets kernel attributes:
  *   make it before any stream capture.
  */

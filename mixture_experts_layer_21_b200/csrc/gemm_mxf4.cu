@@ -658,10 +658,11 @@ cudaError_t run_mxf4_bt(const Mxf4Problem& p, const CUtensorMap& tw, const Mxf4A
     return p.row_idx ? run_mxf4<BT, !PAIR, PAIR>(ta, tw, a, st, pdl) : run_mxf4<BT, false, PAIR>(ta, tw, a, st, pdl);
 }
 
-// The rows that row_idx names, copied into segment order, a warp to a row: where the product runs on CTA
-// pairs a row's codes are read once for every 256 weight rows, and the product of rows in order is faster
-// by more than the copy takes (8192 rows x 4096 into 14336: 246 us against 289, the copy 6). Rows behind
-// the segments are left out: their row_idx may be anything.
+// The rows that row_idx names, copied into segment order, a warp to a row: a product in tiles of 64 tokens
+// and more gains more from rows in order than the copy takes, which is about 3 us (8192 rows x 4096 into
+// 14336 on pairs: 250 us; gathered by four warps of each CTA 289. 128 experts x 2880 x 2880 with 64 rows
+// each 121 and 140, with 32 rows 102 and 107, with 8 rows 98 and 95). Rows behind the segments are left
+// out: their row_idx may be anything.
 __global__ void __launch_bounds__(256) gather_mxfp4_rows_kernel(const uint8_t* __restrict__ codes,
                                                                 const uint8_t* __restrict__ scales, int a_rows,
                                                                 const int32_t* __restrict__ row_idx,
@@ -697,7 +698,7 @@ __global__ void __launch_bounds__(256) gather_mxfp4_rows_kernel(const uint8_t* _
 // 128-token tiles, with 1024 rows 246 and 295; with 64 rows 53 and 49.
 // MOE_TOKEN_TILE=16|32|64|128 and MOE_GEMM_PAIRS=0|1 override the choice (tests, tuning).
 // Returns 16, 32, 64 or 128, or, where rows are in segment order or can be brought into it, kPairTile.
-constexpr int kPairTile = 192;
+constexpr int kPairTile = 192, kOrderedTile = 64;  // kOrderedTile: from here on rows are gathered first
 int mxf4_tile(int G, int N, int M_alloc, bool pairs) {
     const long long segs = std::max<long long>(1, std::min<long long>(G, M_alloc));
     const double avg = (double)M_alloc / (double)segs;
@@ -716,13 +717,13 @@ int mxf4_tile(int G, int N, int M_alloc, bool pairs) {
 }  // namespace
 
 size_t gemm_mxf4_rows_bytes(int G, int N, int K, int M_alloc) {
-    return mxf4_tile(G, N, M_alloc, true) == kPairTile ? (size_t)M_alloc * (K / 2 + K / 32) : 0;
+    return mxf4_tile(G, N, M_alloc, true) >= kOrderedTile ? (size_t)M_alloc * (K / 2 + K / 32) : 0;
 }
 
 cudaError_t launch_gemm_mxf4(const Mxf4Problem& problem, cudaStream_t st, bool pdl) {
     Mxf4Problem p = problem;
     const int bt = mxf4_tile(p.G, p.N, p.M_alloc, !p.row_idx || p.rows);
-    if (bt == kPairTile && p.row_idx) {
+    if (bt >= kOrderedTile && p.row_idx && p.rows) {
         uint8_t* codes = static_cast<uint8_t*>(p.rows);
         uint8_t* scales = codes + (size_t)p.M_alloc * (p.K / 2);
         const cudaError_t e = launch_k(gather_mxfp4_rows_kernel, dim3((p.M_alloc - 1) / 8 + 1), dim3(256), 0, st, pdl, p.a_codes,
