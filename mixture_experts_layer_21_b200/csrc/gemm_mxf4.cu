@@ -29,13 +29,13 @@
 //   epilogue   four warps: tensor memory -> alpha, bf16 -> out
 //   scales     four warps, taking the stages in turn: both sides' scale blocks into the scale ring
 //   gather     four warps, likewise (with row_idx): the token rows' codes by cp.async
-// Barriers, all with bounded waits as in the other GEMMs (s stage, d scale-ring entry, t slot, b buffer):
-//   full[s]      the TMA copies of stage s landed (PAIR: on the leader, both CTAs' copies)
+// Barriers, all with bounded waits as in the other GEMMs (s stage, d scale-ring entry, b buffer):
+//   full[s]      the TMA copies of stage s landed and its scales are in tensor memory (PAIR: on the
+//                leader, both CTAs' copies)
 //   gfull[s]     the gathered rows of stage s landed
-//   empty[s]     the MMAs that read stage s completed (both CTAs)
+//   empty[s]     the MMAs that read stage s, and its slot of scales, completed (both CTAs)
 //   sf_ready[d]  this CTA's scale blocks are in the ring; psf[d], on the leader: the peer's
 //   sf_free[d]   they were copied (both CTAs)
-//   sf_full[t]   the scales are in tensor memory;  slot_free[t]  their MMAs completed
 //   tfull[b]     accumulator b holds a finished tile (both CTAs);  tempty[b]  it was read (leader)
 #include <cmath>
 
@@ -58,7 +58,7 @@ constexpr int kTileRing = 32;
 struct Mxf4Ctl {
     CtrlBlock c;
     int rows[kTileRing];  // rows of this CTA's tiles, written by the producer before the tile's first stage
-    uint64_t gfull[kMaxStages], sf_ready[kSfRing], psf[kSfRing], sf_free[kSfRing], sf_full[kSfRing], slot_free[kSfRing];
+    uint64_t gfull[kMaxStages], sf_ready[kSfRing], psf[kSfRing], sf_free[kSfRing];
 };
 
 // A position in a ring of n entries and the parity of the current turn.
@@ -99,14 +99,16 @@ struct Mxf4Cfg {
     static constexpr int SF_ENTRY = 1024 + 2 * RG * 512;        // weights' two blocks, tokens' [128-K half][row group]
     static constexpr int SF_SLOT = 8 + 8 * RG;                  // TMEM columns of a stage's scales
     static constexpr int SF_BASE = 2 * BT;                      // after two accumulators
-    static constexpr int SLOTS = cmin(kSfRing, (512 - SF_BASE) / SF_SLOT);
-    static constexpr int TMEM_COLS = tmem_cols_pow2(SF_BASE + SLOTS * SF_SLOT);
     // behind the stages: the scale ring, the control block, the gather warps' row tables, the epilogue's staging
     static constexpr int TAB_OFF = (sizeof(Mxf4Ctl) + 15) / 16 * 16;
     static constexpr int STAGING_OFF = (TAB_OFF + (GATHER ? kGatherWarps * B_ROWS * 4 : 0) + 127) / 128 * 128;
     static constexpr int TAIL_BYTES = kSfRing * SF_ENTRY + STAGING_OFF + 4 * 2048;
     static constexpr int STAGES = cmin(kMaxStages, (kSmemLimit - 1024 - TAIL_BYTES) / STAGE);
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE + TAIL_BYTES;
+    // Slots in tensor memory, no more than stages: when the copier takes a slot up again, the MMAs of the
+    // stage that had it have completed, and with them those of the turn of full[s] before its own.
+    static constexpr int SLOTS = cmin(cmin(kSfRing, STAGES), (512 - SF_BASE) / SF_SLOT);
+    static constexpr int TMEM_COLS = tmem_cols_pow2(SF_BASE + SLOTS * SF_SLOT);
     static constexpr int COPIER_WARP = 2;
     static constexpr int EPI_WARP0 = COPIER_WARP + 1;
     static constexpr int SCALE_WARP0 = EPI_WARP0 + 4;
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&ctl->full[s], 1);
+            mbar_init(&ctl->full[s], 2);  // the producer and the copier
             mbar_init(&ctl->empty[s], 1);
             mbar_init(&mc->gfull[s], 32);  // the lanes of the gather warp that copied the stage's rows
         }
@@ -198,8 +200,6 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             mbar_init(&mc->sf_ready[d], 2);  // the weights' copy and the tokens' scale warp
             mbar_init(&mc->psf[d], 1);
             mbar_init(&mc->sf_free[d], 1);
-            mbar_init(&mc->sf_full[d], 1);
-            mbar_init(&mc->slot_free[d], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl->tfull[b], 1);
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             Ring st, sl;
             int b = 0, n = 0;
             uint32_t bph = 0, idesc = 0;
-            bool ok = true, next_sf = false, next_full = false, next_g = !GATHER;
+            bool ok = true, next_full = false, next_g = !GATHER;
             for (int L = first_tile; L < total && ok; L += tile_step, ++n) {
                 if (!wait(&ctl->tempty[b], bph ^ 1u)) {
                     ok = false;
@@ -299,8 +299,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                 }
                 const uint32_t d = tmem_base + (uint32_t)(b * BT);
                 for (int kb = 0; kb < KB; ++kb) {
-                    if ((!next_sf && !wait(&mc->sf_full[sl.i], sl.ph)) || (!next_full && !wait(&ctl->full[st.i], st.ph)) ||
-                        (!next_g && !wait(&mc->gfull[st.i], st.ph))) {
+                    if ((!next_full && !wait(&ctl->full[st.i], st.ph)) || (!next_g && !wait(&mc->gfull[st.i], st.ph))) {
                         ok = false;
                         break;
                     }
@@ -313,7 +312,6 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                     st.next(C::STAGES);
                     sl.next(C::SLOTS);
                     // a look at the next stage's barriers, whose answers come while the MMAs are issued
-                    next_sf = mbar_test(&mc->sf_full[sl.i], sl.ph);
                     next_full = mbar_test(&ctl->full[st.i], st.ph);
                     if (GATHER) next_g = mbar_test(&mc->gfull[st.i], st.ph);
                     const uint64_t as = a0 + (uint64_t)(s * (C::STAGE >> 4)), bs = b0 + (uint64_t)(s * (C::STAGE >> 4));
@@ -332,9 +330,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                         }
                         is.tc = true;
                         commit(&ctl->empty[s]);
-                        commit_here(&mc->slot_free[t]);
                     }
-                    next_sf = __all_sync(0xffffffffu, next_sf);
                     next_full = __all_sync(0xffffffffu, next_full);
                     if (GATHER) next_g = __all_sync(0xffffffffu, next_g);
                 }
@@ -348,15 +344,18 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
     } else if (warp == C::COPIER_WARP) {
         // ---------------- scale blocks: ring -> tensor memory (peer: tells the leader they are in its ring)
         const uint64_t ring0 = sf_block_desc(smem_u32(sf_ring));
-        Ring rg, sl;
+        // st: the stage that the scales are of; last: the stage that had the slot before, SLOTS ago
+        Ring rg, sl, st, last;
+        int it = 0;
         bool ok = true;
         for (int L = first_tile; L < total && ok; L += tile_step) {
             int g, nt, row0, rows;
             tile(L, g, nt, row0, rows);
             const bool wide = C::RG > 1 && mma_n(rows) > 128;  // the second 128-row group is in use
-            for (int kb = 0; kb < KB; ++kb) {
+            for (int kb = 0; kb < KB; ++kb, ++it) {
                 if (!wait(&mc->sf_ready[rg.i], rg.ph) ||
-                    (leader && ((PAIR && !wait(&mc->psf[rg.i], rg.ph)) || !wait(&mc->slot_free[sl.i], sl.ph ^ 1u)))) {
+                    (leader && ((PAIR && !wait(&mc->psf[rg.i], rg.ph)) ||
+                                (it >= C::SLOTS && !wait(&ctl->empty[last.i], last.ph))))) {
                     ok = false;
                     break;
                 }
@@ -381,12 +380,14 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                             }
                         }
                         is.tc = true;
-                        commit_here(&mc->sf_full[sl.i]);
+                        commit_here(&ctl->full[st.i]);
                         commit(&mc->sf_free[rg.i]);
                     }
                 }
                 rg.next(kSfRing);
                 sl.next(C::SLOTS);
+                st.next(C::STAGES);
+                if (it >= C::SLOTS) last.next(C::STAGES);
             }
         }
         if (!ok) give_up(4);
