@@ -25,7 +25,7 @@
 // with one lane elected to issue:
 //   producer   the codes of both sides into the stages (tokens only in segment order)
 //   MMA        a stage's four instructions at most
-//   copier     scale blocks from the scale ring into tensor-memory slots
+//   copier     scale blocks from the scale ring into tensor-memory slots (PAIR: two, taking the stages in turn)
 //   epilogue   four warps: tensor memory -> alpha, bf16 -> out
 //   scales     four warps, taking the stages in turn: both sides' scale blocks into the scale ring
 //   gather     four warps, likewise (with row_idx): the token rows' codes by cp.async
@@ -109,8 +109,11 @@ struct Mxf4Cfg {
     // stage that had it have completed, and with them those of the turn of full[s] before its own.
     static constexpr int SLOTS = cmin(cmin(kSfRing, STAGES), (512 - SF_BASE) / SF_SLOT);
     static constexpr int TMEM_COLS = tmem_cols_pow2(SF_BASE + SLOTS * SF_SLOT);
-    static constexpr int COPIER_WARP = 2;
-    static constexpr int EPI_WARP0 = COPIER_WARP + 1;
+    // A copier's three waits, copies and commits of a stage are about 600 cycles on a pair, where a stage's
+    // MMAs take 350: two take the stages in turn.
+    static constexpr int COPIERS = PAIR ? 2 : 1;
+    static constexpr int COPIER_WARP0 = 2;
+    static constexpr int EPI_WARP0 = COPIER_WARP0 + COPIERS;
     static constexpr int SCALE_WARP0 = EPI_WARP0 + 4;
     static constexpr int GATHER_WARP0 = SCALE_WARP0 + kScaleWarps;
     static constexpr int THREADS = (GATHER_WARP0 + (GATHER ? kGatherWarps : 0)) * 32;
@@ -119,7 +122,7 @@ struct Mxf4Cfg {
     static_assert(STAGES >= 3 && SLOTS >= 2 && SMEM_BYTES <= kSmemLimit && SF_BASE + SLOTS * SF_SLOT <= 512, "MXFP4 GEMM config");
     static_assert(B_BYTES % 1024 == 0, "operand alignment");
     // a warp that takes every n-th turn of a ring finds the turn of an entry before its own finished
-    static_assert((!GATHER || STAGES >= kGatherWarps) && kSfRing % kScaleWarps == 0, "turns of the rings");
+    static_assert((!GATHER || STAGES >= kGatherWarps) && kSfRing % kScaleWarps == 0 && kSfRing % COPIERS == 0, "turns of the rings");
 };
 
 MOE_DEV uint4 ld_shared16(uint32_t addr) {
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             mbar_init(&ctl->tfull[b], 1);
             mbar_init(&ctl->tempty[b], PAIR ? 8 : 4);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&ctl->drain[i], 1);
+        for (int i = 0; i < 1 + C::COPIERS; ++i) mbar_init(&ctl->drain[i], 1);
         ctl->abort = 0;
         fence_barrier_init();
     }
@@ -341,8 +344,10 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             }
             if (!ok) give_up(2);
         }
-    } else if (warp == C::COPIER_WARP) {
-        // ---------------- scale blocks: ring -> tensor memory (peer: tells the leader they are in its ring)
+    } else if (warp < C::EPI_WARP0) {
+        // ---------------- scale blocks: ring -> tensor memory (peer: tells the leader they are in its ring),
+        // every COPIERS-th stage
+        const int mine = warp - C::COPIER_WARP0;
         const uint64_t ring0 = sf_block_desc(smem_u32(sf_ring));
         // st: the stage that the scales are of; last: the stage that had the slot before, SLOTS ago
         Ring rg, sl, st, last;
@@ -353,35 +358,37 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             tile(L, g, nt, row0, rows);
             const bool wide = C::RG > 1 && mma_n(rows) > 128;  // the second 128-row group is in use
             for (int kb = 0; kb < KB; ++kb, ++it) {
-                if (!wait(&mc->sf_ready[rg.i], rg.ph) ||
-                    (leader && ((PAIR && !wait(&mc->psf[rg.i], rg.ph)) ||
-                                (it >= C::SLOTS && !wait(&ctl->empty[last.i], last.ph))))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t src = ring0 + (uint64_t)(rg.i * (C::SF_ENTRY >> 4));
-                const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + sl.i * C::SF_SLOT), sfb = sfa + 8;
-                const bool both = a.KS - 2 * kb > 1;  // both 128-K halves
-                auto copy = [](uint32_t t, uint64_t desc) {
-                    if (PAIR) tmem_cp_32x128b_x4_pair(t, desc);
-                    else tmem_cp_32x128b_x4(t, desc);
-                };
-                if (elect_one()) {
-                    if (!leader) {
-                        mbar_arrive_remote(mapa_shared(smem_u32(&mc->psf[rg.i]), 0));
-                    } else {
+                if (C::COPIERS == 1 || it % C::COPIERS == mine) {
+                    if (!wait(&mc->sf_ready[rg.i], rg.ph) ||
+                        (leader && ((PAIR && !wait(&mc->psf[rg.i], rg.ph)) ||
+                                    (it >= C::SLOTS && !wait(&ctl->empty[last.i], last.ph))))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t src = ring0 + (uint64_t)(rg.i * (C::SF_ENTRY >> 4));
+                    const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + sl.i * C::SF_SLOT), sfb = sfa + 8;
+                    const bool both = a.KS - 2 * kb > 1;  // both 128-K halves
+                    auto copy = [](uint32_t t, uint64_t desc) {
+                        if (PAIR) tmem_cp_32x128b_x4_pair(t, desc);
+                        else tmem_cp_32x128b_x4(t, desc);
+                    };
+                    if (elect_one()) {
+                        if (!leader) {
+                            mbar_arrive_remote(mapa_shared(smem_u32(&mc->psf[rg.i]), 0));
+                        } else {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (h == 0 || both) {
-                                copy(sfa + 4 * h, src + 32 * h);
-                                copy(sfb + 4 * h * C::RG, src + 64 + 32 * h * C::RG);
-                                if (wide) copy(sfb + 4 * (h * C::RG + 1), src + 64 + 32 * (h * C::RG + 1));
+                            for (int h = 0; h < 2; ++h) {
+                                if (h == 0 || both) {
+                                    copy(sfa + 4 * h, src + 32 * h);
+                                    copy(sfb + 4 * h * C::RG, src + 64 + 32 * h * C::RG);
+                                    if (wide) copy(sfb + 4 * (h * C::RG + 1), src + 64 + 32 * (h * C::RG + 1));
+                                }
                             }
+                            is.tc = true;
+                            commit_here(&ctl->full[st.i]);
+                            commit(&mc->sf_free[rg.i]);
                         }
-                        is.tc = true;
-                        commit_here(&ctl->full[st.i]);
-                        commit(&mc->sf_free[rg.i]);
                     }
                 }
                 rg.next(kSfRing);
