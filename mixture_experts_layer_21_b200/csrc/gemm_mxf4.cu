@@ -27,8 +27,9 @@
 //   MMA        a stage's four instructions at most
 //   copier     scale blocks from the scale ring into tensor-memory slots (PAIR: two, taking the stages in turn)
 //   epilogue   four warps: tensor memory -> alpha, bf16 -> out
-//   scales     four warps, taking the stages in turn: both sides' scale blocks into the scale ring
-//   gather     four warps, likewise (with row_idx): the token rows' codes by cp.async
+//   scales     eight warps (four with row_idx), taking the stages in turn: both sides' scale blocks into the
+//              scale ring
+//   gather     four warps, in turn too (with row_idx): the token rows' codes by cp.async
 // Barriers, all with bounded waits as in the other GEMMs (s stage, d scale-ring entry, b buffer):
 //   full[s]      the TMA copies of stage s landed and its scales are in tensor memory (PAIR: on the
 //                leader, both CTAs' copies)
@@ -46,7 +47,6 @@ namespace moe {
 namespace {
 
 constexpr int kStageK = 256;
-constexpr int kScaleWarps = 4;
 constexpr int kGatherWarps = 4;
 constexpr int kSfRing = 8;
 
@@ -115,14 +115,18 @@ struct Mxf4Cfg {
     static constexpr int COPIER_WARP0 = 2;
     static constexpr int EPI_WARP0 = COPIER_WARP0 + COPIERS;
     static constexpr int SCALE_WARP0 = EPI_WARP0 + 4;
-    static constexpr int GATHER_WARP0 = SCALE_WARP0 + kScaleWarps;
+    // A scale warp spends about 2400 cycles on a stage, most of them on its loads' way; with four warps that
+    // was 630 (pairs) and 540 cycles a stage, the pace of the whole kernel. (Gathered rows of short segments
+    // wait for the weights.)
+    static constexpr int SCALE_WARPS = GATHER ? 4 : 8;
+    static constexpr int GATHER_WARP0 = SCALE_WARP0 + SCALE_WARPS;
     static constexpr int THREADS = (GATHER_WARP0 + (GATHER ? kGatherWarps : 0)) * 32;
     static_assert(BT % 16 == 0 && BT >= 16 && BT <= 240, "token tile");
     static_assert(!PAIR || (BT % 32 == 0 && !GATHER), "pair MMA N: a multiple of 32; tokens by TMA");
     static_assert(STAGES >= 3 && SLOTS >= 2 && SMEM_BYTES <= kSmemLimit && SF_BASE + SLOTS * SF_SLOT <= 512, "MXFP4 GEMM config");
     static_assert(B_BYTES % 1024 == 0, "operand alignment");
     // a warp that takes every n-th turn of a ring finds the turn of an entry before its own finished
-    static_assert((!GATHER || STAGES >= kGatherWarps) && kSfRing % kScaleWarps == 0 && kSfRing % COPIERS == 0, "turns of the rings");
+    static_assert((!GATHER || STAGES >= kGatherWarps) && kSfRing % SCALE_WARPS == 0 && kSfRing % COPIERS == 0, "turns of the rings");
 };
 
 MOE_DEV uint4 ld_shared16(uint32_t addr) {
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
         for (long long i = (long long)blockIdx.x * 128 + threadIdx.x - 32 * C::EPI_WARP0; i < n8; i += (long long)gridDim.x * 128)
             o[i] = make_uint4(0u, 0u, 0u, 0u);
     } else if (warp < C::GATHER_WARP0) {
-        // ---------------- scale warp: every kScaleWarps-th stage
+        // ---------------- scale warp: every SCALE_WARPS-th stage
         constexpr int NR = (BT + 31) / 32;  // rows per lane: lane, lane + 32, ...
         const int mine = warp - C::SCALE_WARP0;
         const int row_bytes = a.K / 32;
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                 }
             }
             for (int kb = 0; kb < KB; ++kb, ++it) {
-                if (it % kScaleWarps == mine) {
+                if (it % C::SCALE_WARPS == mine) {
                     const int d = rg.i;
                     uint2 v[4 * C::RG];
 #pragma unroll
