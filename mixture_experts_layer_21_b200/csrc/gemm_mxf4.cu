@@ -27,8 +27,7 @@
 //   MMA        a stage's four instructions at most
 //   copier     scale blocks from the scale ring into tensor-memory slots (PAIR: two, taking the stages in turn)
 //   epilogue   four warps: tensor memory -> alpha, bf16 -> out
-//   scales     eight warps (four with row_idx), taking the stages in turn: both sides' scale blocks into the
-//              scale ring
+//   scales     four or eight warps, taking the stages in turn: both sides' scale blocks into the scale ring
 //   gather     four warps, in turn too (with row_idx): the token rows' codes by cp.async
 // Barriers, all with bounded waits as in the other GEMMs (s stage, d scale-ring entry, b buffer):
 //   full[s]      the TMA copies of stage s landed and its scales are in tensor memory (PAIR: on the
@@ -116,9 +115,10 @@ struct Mxf4Cfg {
     static constexpr int EPI_WARP0 = COPIER_WARP0 + COPIERS;
     static constexpr int SCALE_WARP0 = EPI_WARP0 + 4;
     // A scale warp spends about 2400 cycles on a stage, most of them on its loads' way; with four warps that
-    // was 630 (pairs) and 540 cycles a stage, the pace of the whole kernel. (Gathered rows of short segments
-    // wait for the weights.)
-    static constexpr int SCALE_WARPS = GATHER ? 4 : 8;
+    // was 630 (pairs) and 540 cycles a stage, the pace of the whole kernel (128 experts x 2880 x 2880 with 64
+    // rows each: 118 us, with eight warps 104). Smaller tiles wait for the weights from memory, and four are
+    // better there (with 32 rows each 98 us against 101).
+    static constexpr int SCALE_WARPS = GATHER || BT < 128 ? 4 : 8;
     static constexpr int GATHER_WARP0 = SCALE_WARP0 + SCALE_WARPS;
     static constexpr int THREADS = (GATHER_WARP0 + (GATHER ? kGatherWarps : 0)) * 32;
     static_assert(BT % 16 == 0 && BT >= 16 && BT <= 240, "token tile");
