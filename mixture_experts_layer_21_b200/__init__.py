@@ -436,7 +436,8 @@ def moe_grouped_gemm_mxfp4(a_codes: torch.Tensor, a_scales: torch.Tensor, w: Wei
                            row_idx=None, out=None, ws=None, stream=None) -> torch.Tensor:
     """Block-scaled grouped GEMM on MXFP4 activations (codes [R,K/2], e8m0 scales [R,K/32]) and
     prepared MXFP4 weights. row_idx (int32 [M]): row r of the segments is row row_idx[r] of a (the
-    permutation's perm_token); without it the R rows are in segment order. bf16 out [M,N]."""
+    permutation's perm_token), segments of many rows being gathered before the product into memory
+    allocated here; without it the R rows are in segment order. bf16 out [M,N]."""
     R, dev, u8 = a_codes.shape[0], _launch_device(a_codes), torch.uint8
     K, N = w.K, w.N
     _want(a_codes, "a_codes", (R, K // 2), u8, dev)

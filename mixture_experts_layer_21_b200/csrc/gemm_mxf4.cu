@@ -672,7 +672,7 @@ cudaError_t run_mxf4_bt(const Mxf4Problem& p, const CUtensorMap& tw, const Mxf4A
 
 // The rows that row_idx names, copied into segment order, a warp to a row: a product in tiles of 64 tokens
 // and more gains more from rows in order than the copy takes, which is about 3 us (8192 rows x 4096 into
-// 14336 on pairs: 250 us; gathered by four warps of each CTA 289. 128 experts x 2880 x 2880 with 64 rows
+// 14336 on pairs: 250 us when gathering in the product took 289. 128 experts x 2880 x 2880 with 64 rows
 // each 121 and 140, with 32 rows 102 and 107, with 8 rows 98 and 95). Rows behind the segments are left
 // out: their row_idx may be anything.
 __global__ void __launch_bounds__(256) gather_mxfp4_rows_kernel(const uint8_t* __restrict__ codes,
@@ -706,8 +706,8 @@ __global__ void __launch_bounds__(256) gather_mxfp4_rows_kernel(const uint8_t* _
 
 // Token tile: a tile costs a stage per 256 K whatever its width, so it should hold a whole segment;
 // mean + 2 sqrt(mean) covers nearly every one. Longer segments go to CTA pairs, where there is a
-// tile for each pair of SMs: 8 experts x 14336 x 4096 with 128 rows each took 56 us on pairs, 59 in
-// 128-token tiles, with 1024 rows 246 and 295; with 64 rows 53 and 49.
+// tile for each pair of SMs: 8 experts x 14336 x 4096 with 128 rows each took 55 us on pairs, 57 in
+// 128-token tiles, with 1024 rows 228 and 263; with 64 rows 51 and 49.
 // MOE_TOKEN_TILE=16|32|64|128 and MOE_GEMM_PAIRS=0|1 override the choice (tests, tuning).
 // Returns 16, 32, 64 or 128, or, where rows are in segment order or can be brought into it, kPairTile.
 constexpr int kPairTile = 192, kOrderedTile = 64;  // kOrderedTile: from here on rows are gathered first
