@@ -57,22 +57,29 @@ __device__ __forceinline__ void decode_tile(int L, const CtrlBlock* c, int G, in
     rows = min(rs, c->cu[g] - row0);
 }
 
-// One warp: the segment table (cu, clamped, and the running tile count tpre).
-// Ends are clamped to [0, M_alloc] and a segment whose end lies before the previous
-// end counts as empty, so no tile can touch rows outside the buffers.
+// One warp: the segment table (cu, the running maximum of the ends clamped to [0, M_alloc], and the
+// running tile count tpre). A segment whose end lies before an earlier one is empty, and the next begins
+// where the longest so far ended: every tile has rows, inside the buffers, and no two share one. (Taken
+// from the given end before it, a segment after one that fell could get more tiles than rows, and an MMA
+// of width 0 with them.)
 template <int BT, typename Args>
 __device__ __forceinline__ void build_segment_table(const Args& a, CtrlBlock* ctl, int lane) {
     const int G = a.G, NT = a.NT;
-    int carry = 0, prev_chunk_end = 0;
+    int carry = 0, before = 0;  // tiles, and the running maximum, up to this chunk of 32 segments
     for (int base = 0; base < G; base += 32) {
         const int g = base + lane;
         const int raw = g < G ? a.cu[g] : 0;
-        const int end = min(max(raw, 0), a.M_alloc);
+        const int own = min(max(raw, 0), a.M_alloc);
+        int end = max(own, before);
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, end, off);
+            if (lane >= off) end = max(end, n);
+        }
         int prev = __shfl_up_sync(0xffffffffu, end, 1);
-        if (lane == 0) prev = prev_chunk_end;
-        if (g < G && (raw != end || end < prev)) report_error(a.err, MOE_ERR_DEVICE, 1000000 + g);
-        const int len = g < G ? max(0, end - prev) : 0;
-        const int tiles = ((len + BT - 1) / BT) * NT;
+        if (lane == 0) prev = before;
+        if (g < G && (raw != own || own < prev)) report_error(a.err, MOE_ERR_DEVICE, 1000000 + g);
+        const int tiles = ((end - prev + BT - 1) / BT) * NT;  // 0 past the last segment, whose own end is 0
         int incl = tiles;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -80,12 +87,11 @@ __device__ __forceinline__ void build_segment_table(const Args& a, CtrlBlock* ct
             if (lane >= off) incl += n;
         }
         if (g < G) {
-            ctl->cu[g] = len > 0 ? end : prev;
+            ctl->cu[g] = end;
             ctl->tpre[g + 1] = carry + incl;
         }
         carry += __shfl_sync(0xffffffffu, incl, 31);
-        const int eff = g < G ? (len > 0 ? end : prev) : prev;
-        prev_chunk_end = __shfl_sync(0xffffffffu, eff, 31);
+        before = __shfl_sync(0xffffffffu, end, 31);
     }
     if (lane == 0) ctl->tpre[0] = 0;
 }
