@@ -432,16 +432,25 @@ moe_status_t moe_quantize_mxfp4(const void* in, int in_is_f32, int64_t in_stride
  *   w       MXFP4 weights prepared by moe_prepare_weights (else NOT_PREPARED); other formats:
  *           UNSUPPORTED.
  *   out bf16 [M_alloc, N], N % 8 == 0; cu_seqlens int32 [G] on device; G <= 1024.
- *   rows: with row_idx, room for moe_grouped_gemm_mxfp4_rows_size bytes (16-byte aligned), into which
- *           segments of many rows are gathered before their product, or NULL: the product gathers
- *           them as it goes, slower for such segments. The size is 0 where it is not used.
  *   ws: at least 256 bytes (the error word). The first call on a device sets kernel attributes:
  *   make it before any stream capture.
+ *   rows: NULL. (It took memory for gathered rows without its size; a pointer is refused with
+ *   MOE_ERR_INVALID_ARG.)
+ * moe_grouped_gemm_mxfp4_room is the same call with memory for gathered rows:
+ *   rows: rows_bytes bytes, 16-byte aligned, into which segments of many rows are gathered before
+ *           their product, or NULL: the product gathers them as it goes, slower for such segments.
+ *           moe_grouped_gemm_mxfp4_rows_size gives the bytes that a call of this M_alloc and w
+ *           takes under the present MOE_TOKEN_TILE and MOE_GEMM_PAIRS, 0 where it takes none;
+ *           fewer: MOE_ERR_WORKSPACE_TOO_SMALL. Without row_idx it is not used.
  */
 moe_status_t moe_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int a_rows,
                                     const int32_t* row_idx, int M_alloc, const moe_weight_t* w,
                                     const int32_t* cu_seqlens, void* out, void* rows, void* ws, size_t ws_bytes,
                                     moe_stream_t stream);
+moe_status_t moe_grouped_gemm_mxfp4_room(const uint8_t* a_codes, const uint8_t* a_scales, int a_rows,
+                                         const int32_t* row_idx, int M_alloc, const moe_weight_t* w,
+                                         const int32_t* cu_seqlens, void* out, void* rows, size_t rows_bytes,
+                                         void* ws, size_t ws_bytes, moe_stream_t stream);
 size_t moe_grouped_gemm_mxfp4_rows_size(int M_alloc, const moe_weight_t* w);
 
 /*

@@ -42,7 +42,8 @@ EXPORTS = ["moe_status_string", "moe_version", "moe_route_topk", "moe_permute_wo
            "moe_forward_workspace_size", "moe_forward", "moe_get_device_error", "moe_permute_noalloc",
            "moe_permute_noalloc_status", "moe_grouped_gemm_nvfp4", "moe_quantize_mxfp8", "moe_route_topk_grouped",
            "moe_bias_act_and_mul", "moe_forward_workspace_size_args", "moe_route_scored", "moe_add_rmsnorm",
-           "moe_quantize_mxfp4", "moe_grouped_gemm_mxfp4", "moe_grouped_gemm_mxfp4_rows_size"]
+           "moe_quantize_mxfp4", "moe_grouped_gemm_mxfp4", "moe_grouped_gemm_mxfp4_room",
+           "moe_grouped_gemm_mxfp4_rows_size"]
 
 
 class MoEError(RuntimeError):
@@ -146,6 +147,7 @@ _sig = {
     "moe_add_rmsnorm": (_I, [_P, _P]),       # moe_rmsnorm_args_t*
     "moe_quantize_mxfp4": (_I, [_P, _I, _L, _I, _I, _P, _P, _P, _P]),
     "moe_grouped_gemm_mxfp4": (_I, [_P, _P, _I, _P, _I, ctypes.POINTER(moe_weight_t), _P, _P, _P, _P, _S, _P]),
+    "moe_grouped_gemm_mxfp4_room": (_I, [_P, _P, _I, _P, _I, ctypes.POINTER(moe_weight_t), _P, _P, _P, _S, _P, _S, _P]),
     "moe_grouped_gemm_mxfp4_rows_size": (_S, [_I, ctypes.POINTER(moe_weight_t)]),
 }
 for _name, (_res, _args) in _sig.items():
@@ -445,7 +447,7 @@ def moe_grouped_gemm_mxfp4(a_codes: torch.Tensor, a_scales: torch.Tensor, w: Wei
     _want(cu_seqlens, "cu_seqlens", (w.G,), torch.int32, dev)
     if w.data.get_device() != dev:
         raise ValueError(f"w: need weights on cuda:{dev}, got {w.data.device}")
-    M, rows = R, None
+    M, rows, room = R, None, 0
     if row_idx is not None:
         M = row_idx.shape[0]
         _want(row_idx, "row_idx", (M,), torch.int32, dev)
@@ -461,9 +463,9 @@ def moe_grouped_gemm_mxfp4(a_codes: torch.Tensor, a_scales: torch.Tensor, w: Wei
         ws = torch.zeros(256, dtype=u8, device=a_codes.device)
     elif ws.get_device() != dev:
         raise ValueError(f"ws: need a workspace on cuda:{dev}, got {ws.device}")
-    _check(_lib.moe_grouped_gemm_mxfp4(a_codes.data_ptr(), a_scales.data_ptr(), R, _ptr(row_idx), M, w.desc_ref,
-                                       cu_seqlens.data_ptr(), out.data_ptr(), _ptr(rows), ws.data_ptr(), ws.numel(),
-                                       _launch_stream(dev, stream)), "moe_grouped_gemm_mxfp4")
+    _check(_lib.moe_grouped_gemm_mxfp4_room(a_codes.data_ptr(), a_scales.data_ptr(), R, _ptr(row_idx), M, w.desc_ref,
+                                            cu_seqlens.data_ptr(), out.data_ptr(), _ptr(rows), room, ws.data_ptr(),
+                                            ws.numel(), _launch_stream(dev, stream)), "moe_grouped_gemm_mxfp4")
     return out
 
 

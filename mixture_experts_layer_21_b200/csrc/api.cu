@@ -270,12 +270,13 @@ moe_status_t moe_quantize_mxfp4(const void* in, int in_is_f32, int64_t in_stride
 
 size_t moe_grouped_gemm_mxfp4_rows_size(int M_alloc, const moe_weight_t* w) {
     if (!w || M_alloc < 1 || w->G < 1 || w->N < 1 || w->K < 1) return 0;
-    return gemm_mxf4_rows_bytes(w->G, w->N, w->K, M_alloc);
+    return gemm_mxf4_rows_bytes(gemm_mxf4_tile(w->G, w->N, M_alloc, true), w->K, M_alloc);
 }
 
-moe_status_t moe_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int a_rows, const int32_t* row_idx,
-                                    int M_alloc, const moe_weight_t* w, const int32_t* cu_seqlens, void* out, void* rows,
-                                    void* ws, size_t ws_bytes, moe_stream_t stream) {
+moe_status_t moe_grouped_gemm_mxfp4_room(const uint8_t* a_codes, const uint8_t* a_scales, int a_rows,
+                                         const int32_t* row_idx, int M_alloc, const moe_weight_t* w,
+                                         const int32_t* cu_seqlens, void* out, void* rows, size_t rows_bytes, void* ws,
+                                         size_t ws_bytes, moe_stream_t stream) {
     if (!w || M_alloc < 0 || a_rows < 0 || w->G < 1 || w->N < 1 || w->K < 1) return MOE_ERR_INVALID_ARG;
     if (w->G > 1024) return MOE_ERR_UNSUPPORTED;
     if (w->fmt != MOE_W_MXFP4) return MOE_ERR_UNSUPPORTED;
@@ -286,10 +287,21 @@ moe_status_t moe_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_sca
     if (!a_codes || !a_scales || !cu_seqlens || !out || !ws) return MOE_ERR_INVALID_ARG;
     if (!aligned16(a_codes) || !aligned16(out) || !aligned16(rows) || w->N % 8) return MOE_ERR_ALIGNMENT;
     if (ws_bytes < kErrBytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    // the tile is chosen once: the room is checked for the launch that uses it
+    const int tile = gemm_mxf4_tile(w->G, w->N, M_alloc, !row_idx || rows);
+    if (row_idx && rows && rows_bytes < gemm_mxf4_rows_bytes(tile, w->K, M_alloc)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     const Mxf4Problem p{a_codes,   a_scales,  a_rows,          row_idx,    M_alloc, w->G, w->N, w->K,
                         w->kdata,  w->kscale, weight_alpha(*w), cu_seqlens, out,     reinterpret_cast<DevError*>(ws),
-                        rows};
+                        rows,      tile};
     return cuda_status(launch_gemm_mxf4(p, S(stream), false));
+}
+
+moe_status_t moe_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int a_rows, const int32_t* row_idx,
+                                    int M_alloc, const moe_weight_t* w, const int32_t* cu_seqlens, void* out, void* rows,
+                                    void* ws, size_t ws_bytes, moe_stream_t stream) {
+    if (rows) return aligned16(rows) ? MOE_ERR_INVALID_ARG : MOE_ERR_ALIGNMENT;  // its size is not known
+    return moe_grouped_gemm_mxfp4_room(a_codes, a_scales, a_rows, row_idx, M_alloc, w, cu_seqlens, out, nullptr, 0, ws,
+                                       ws_bytes, stream);
 }
 
 size_t moe_permute_workspace_size(int T, int topk, int E, int B) {

@@ -704,14 +704,17 @@ __global__ void __launch_bounds__(256) gather_mxfp4_rows_kernel(const uint8_t* _
     pdl_launch();
 }
 
+constexpr int kPairTile = 192, kOrderedTile = 64;  // kOrderedTile: from here on rows are gathered first
+
+}  // namespace
+
 // Token tile: a tile costs a stage per 256 K whatever its width, so it should hold a whole segment;
 // mean + 2 sqrt(mean) covers nearly every one. Longer segments go to CTA pairs, where there is a
 // tile for each pair of SMs: 8 experts x 14336 x 4096 with 128 rows each took 55 us on pairs, 57 in
 // 128-token tiles, with 1024 rows 228 and 263; with 64 rows 51 and 49.
 // MOE_TOKEN_TILE=16|32|64|128 and MOE_GEMM_PAIRS=0|1 override the choice (tests, tuning).
 // Returns 16, 32, 64 or 128, or, where rows are in segment order or can be brought into it, kPairTile.
-constexpr int kPairTile = 192, kOrderedTile = 64;  // kOrderedTile: from here on rows are gathered first
-int mxf4_tile(int G, int N, int M_alloc, bool pairs) {
+int gemm_mxf4_tile(int G, int N, int M_alloc, bool pairs) {
     const long long segs = std::max<long long>(1, std::min<long long>(G, M_alloc));
     const double avg = (double)M_alloc / (double)segs;
     const char* env = getenv("MOE_TOKEN_TILE");
@@ -726,15 +729,13 @@ int mxf4_tile(int G, int N, int M_alloc, bool pairs) {
     return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
 }
 
-}  // namespace
-
-size_t gemm_mxf4_rows_bytes(int G, int N, int K, int M_alloc) {
-    return mxf4_tile(G, N, M_alloc, true) >= kOrderedTile ? (size_t)M_alloc * (K / 2 + K / 32) : 0;
+size_t gemm_mxf4_rows_bytes(int tile, int K, int M_alloc) {
+    return tile >= kOrderedTile ? (size_t)M_alloc * (K / 2 + K / 32) : 0;
 }
 
 cudaError_t launch_gemm_mxf4(const Mxf4Problem& problem, cudaStream_t st, bool pdl) {
     Mxf4Problem p = problem;
-    const int bt = mxf4_tile(p.G, p.N, p.M_alloc, !p.row_idx || p.rows);
+    const int bt = p.tile;
     if (bt >= kOrderedTile && p.row_idx && p.rows) {
         uint8_t* codes = static_cast<uint8_t*>(p.rows);
         uint8_t* scales = codes + (size_t)p.M_alloc * (p.K / 2);

@@ -189,8 +189,12 @@ struct Mxf4Problem {
     void* out;
     DevError* err;
     void* rows;  // room for the gathered rows (gemm_mxf4_rows_bytes), or null
+    int tile;    // gemm_mxf4_tile
 };
-size_t gemm_mxf4_rows_bytes(int G, int N, int K, int M_alloc);
+// The token tile of a product (pairs: rows are in segment order or there is room to bring them into it),
+// and the bytes of rows that a product in such tiles gathers first.
+int gemm_mxf4_tile(int G, int N, int M_alloc, bool pairs);
+size_t gemm_mxf4_rows_bytes(int tile, int K, int M_alloc);
 cudaError_t launch_gemm_mxf4(const Mxf4Problem& p, cudaStream_t st, bool pdl);
 int choose_token_tile(long long NvS, int G, bool wide_ok);
 
