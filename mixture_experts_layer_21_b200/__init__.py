@@ -168,6 +168,15 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _on(stream, make, *args, **kw) -> torch.Tensor:
+    """A tensor that a call makes for itself or its caller: memory of the stream that the call launches on,
+    filled in that stream's order. A block of the current stream's could still be read or written there."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _check(status: int, where: str) -> None:
     if status != MOE_OK:
         raise MoEError(status, where)
@@ -198,11 +207,11 @@ def _want(t, name: str, shape, dtype, dev: int, dense: bool = True) -> int:
     raise ValueError(f"{name}: need {tuple(shape)} {dtype} on cuda:{dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
-def _output(out, name: str, like, shape, dtype, dev: int, dense: bool = True):
+def _output(out, name: str, like, shape, dtype, dev: int, stream, dense: bool = True):
     """The caller's output of that name, checked, or a new one; and its row stride."""
     t = out.get(name)
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device), 0
+        return _on(stream, torch.empty, shape, dtype=dtype, device=like.device), 0
     return t, _want(t, name, shape, dtype, dev, dense)
 
 
@@ -272,7 +281,7 @@ def moe_prepare_weights(w: Weight, stream=None) -> Weight:
     if w.fmt == "bf16":
         return w
     nbytes = _lib.moe_prepared_weight_bytes(ctypes.byref(w.desc))
-    w.prepared = torch.empty(nbytes, dtype=torch.uint8, device=w.data.device)
+    w.prepared = _on(stream, torch.empty, nbytes, dtype=torch.uint8, device=w.data.device)
     _check(_lib.moe_prepare_weights(ctypes.byref(w.desc), _ptr(w.prepared), nbytes, _stream(stream)),
            "moe_prepare_weights")
     return w
@@ -282,8 +291,8 @@ def moe_prepare_weights(w: Weight, stream=None) -> Weight:
 
 def moe_route_topk(logits: torch.Tensor, topk: int, ids=None, w=None, stream=None):
     T, E = logits.shape
-    ids = ids if ids is not None else torch.empty(T, topk, dtype=torch.int32, device=logits.device)
-    w = w if w is not None else torch.empty(T, topk, dtype=torch.float32, device=logits.device)
+    ids = ids if ids is not None else _on(stream, torch.empty, T, topk, dtype=torch.int32, device=logits.device)
+    w = w if w is not None else _on(stream, torch.empty, T, topk, dtype=torch.float32, device=logits.device)
     _check(_lib.moe_route_topk(_ptr(logits), T, E, topk, _ptr(ids), _ptr(w), _stream(stream)),
            "moe_route_topk")
     return ids, w
@@ -293,8 +302,8 @@ def moe_route_topk_grouped(logits: torch.Tensor, topk: int, n_group: int, topk_g
                            routed_scaling_factor: float = 1.0, ids=None, w=None, stream=None):
     """DeepSeekV3 routing (grouped top-k on sigmoid scores, bias for selection only)."""
     T, E = logits.shape
-    ids = ids if ids is not None else torch.empty(T, topk, dtype=torch.int32, device=logits.device)
-    w = w if w is not None else torch.empty(T, topk, dtype=torch.float32, device=logits.device)
+    ids = ids if ids is not None else _on(stream, torch.empty, T, topk, dtype=torch.int32, device=logits.device)
+    w = w if w is not None else _on(stream, torch.empty, T, topk, dtype=torch.float32, device=logits.device)
     _check(_lib.moe_route_topk_grouped(_ptr(logits), _ptr(bias), T, E, topk, n_group, topk_group,
                                        routed_scaling_factor, _ptr(ids), _ptr(w), _stream(stream)),
            "moe_route_topk_grouped")
@@ -314,11 +323,11 @@ def moe_route_scored(logits: torch.Tensor, topk: int, scoring: str = "softmax", 
     if bias is not None:
         _want(bias, "bias", (E,), torch.float32, dev)
     if ids is None:
-        ids = torch.empty(T, topk, dtype=torch.int32, device=logits.device)
+        ids = _on(stream, torch.empty, T, topk, dtype=torch.int32, device=logits.device)
     else:
         _want(ids, "ids", (T, topk), torch.int32, dev)
     if w is None:
-        w = torch.empty(T, topk, dtype=torch.float32, device=logits.device)
+        w = _on(stream, torch.empty, T, topk, dtype=torch.float32, device=logits.device)
     else:
         _want(w, "w", (T, topk), torch.float32, dev)
     a = _ROUTE_ARGS.pack(logits.data_ptr(), 0 if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr(),
@@ -348,22 +357,22 @@ def moe_add_rmsnorm(x: torch.Tensor, weight=None, residual=None, eps: float = 1e
     sres = sr = sy = pres = pw = pr = py = pc = ps = pd = w32 = 0
     if residual is not None:
         sres, pres = _want(residual, "residual", shape, bf16, dev, False), residual.data_ptr()
-        r, sr = _output(out, "residual", x, shape, bf16, dev, False)
+        r, sr = _output(out, "residual", x, shape, bf16, dev, stream, False)
         pr = r.data_ptr()
     if weight is not None:
         wt = _float_type(weight, "weight")
         _want(weight, "weight", (H,), wt, dev)
         pw, w32 = weight.data_ptr(), wt is not bf16
     if want_y:
-        y, sy = _output(out, "y", x, shape, bf16, dev, False)
+        y, sy = _output(out, "y", x, shape, bf16, dev, stream, False)
         py = y.data_ptr()
     q = QUANT[quant]
     if q:
-        codes, _ = _output(out, "codes", x, (T, H // 2) if q == 2 else shape, torch.uint8, dev)
-        scales, _ = _output(out, "scales", x, (T, H // 32), torch.uint8, dev)
+        codes, _ = _output(out, "codes", x, (T, H // 2) if q == 2 else shape, torch.uint8, dev, stream)
+        scales, _ = _output(out, "scales", x, (T, H // 32), torch.uint8, dev, stream)
         pc, ps = codes.data_ptr(), scales.data_ptr()
         if deq:
-            d, _ = _output(out, "deq", x, shape, bf16, dev)
+            d, _ = _output(out, "deq", x, shape, bf16, dev, stream)
             pd = d.data_ptr()
     elif deq:
         raise ValueError("deq needs quant")
@@ -386,10 +395,10 @@ def moe_permute(topk_ids, topk_w, E: int, B: int = 0, replica_src=None, x=None, 
     NvS = T * k
     out = out or {}
     M_alloc = NvS if M_alloc is None else M_alloc
-    ws = ws if ws is not None else permute_workspace(T, k, E, B, dev)
+    ws = ws if ws is not None else _on(stream, permute_workspace, T, k, E, B, dev)
     def buf(name, shape, dtype):
         t = out.get(name)
-        return t if t is not None else torch.empty(shape, dtype=dtype, device=dev)
+        return t if t is not None else _on(stream, torch.empty, shape, dtype=dtype, device=dev)
 
     cu = buf("cu_seqlens", (E + B,), torch.int32)
     perm_token = buf("perm_token", (NvS,), torch.int32)
@@ -401,7 +410,7 @@ def moe_permute(topk_ids, topk_w, E: int, B: int = 0, replica_src=None, x=None, 
         H = x.shape[1]
         x_perm = out.get("x_perm")
         if x_perm is None:
-            x_perm = torch.zeros(M_alloc, H, dtype=x.dtype, device=dev)
+            x_perm = _on(stream, torch.zeros, M_alloc, H, dtype=x.dtype, device=dev)
         M_alloc = x_perm.shape[0]
     _check(_lib.moe_permute(_ptr(topk_ids), _ptr(topk_w), T, k, E, B, _ptr(replica_src), _ptr(x), H,
                             _ptr(cu), _ptr(perm_token), _ptr(perm_w), _ptr(inv), _ptr(x_perm), M_alloc,
@@ -412,10 +421,10 @@ def moe_permute(topk_ids, topk_w, E: int, B: int = 0, replica_src=None, x=None, 
 def moe_grouped_gemm(a: torch.Tensor, w: Weight, cu_seqlens: torch.Tensor, out=None, ws=None,
                      stream=None) -> torch.Tensor:
     M = a.shape[0]
-    out = out if out is not None else torch.empty(M, w.N, dtype=torch.bfloat16, device=a.device)
+    out = out if out is not None else _on(stream, torch.empty, M, w.N, dtype=torch.bfloat16, device=a.device)
     if ws is None:
         n = _lib.moe_grouped_gemm_workspace_size(M, ctypes.byref(w.desc))
-        ws = torch.zeros(n, dtype=torch.uint8, device=a.device)
+        ws = _on(stream, torch.zeros, n, dtype=torch.uint8, device=a.device)
     _check(_lib.moe_grouped_gemm(_ptr(a), M, ctypes.byref(w.desc), _ptr(cu_seqlens), _ptr(out),
                                  _ptr(ws), ws.numel(), _stream(stream)), "moe_grouped_gemm")
     return out
@@ -426,8 +435,8 @@ def moe_grouped_gemm_nvfp4(a_codes: torch.Tensor, a_sb: torch.Tensor, a_s: torch
     """Block-scaled grouped GEMM on NVFP4 activations (codes [M,K/2], e4m3 scales [M,K/16],
     row scales [M]) and prepared NVFP4 weights; bf16 out [M,N]."""
     M = a_codes.shape[0]
-    out = out if out is not None else torch.empty(M, w.N, dtype=torch.bfloat16, device=a_codes.device)
-    ws = ws if ws is not None else torch.zeros(256, dtype=torch.uint8, device=a_codes.device)
+    out = out if out is not None else _on(stream, torch.empty, M, w.N, dtype=torch.bfloat16, device=a_codes.device)
+    ws = ws if ws is not None else _on(stream, torch.zeros, 256, dtype=torch.uint8, device=a_codes.device)
     _check(_lib.moe_grouped_gemm_nvfp4(_ptr(a_codes), _ptr(a_sb), _ptr(a_s), M, ctypes.byref(w.desc),
                                        _ptr(cu_seqlens), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
            "moe_grouped_gemm_nvfp4")
@@ -453,14 +462,13 @@ def moe_grouped_gemm_mxfp4(a_codes: torch.Tensor, a_scales: torch.Tensor, w: Wei
         _want(row_idx, "row_idx", (M,), torch.int32, dev)
         room = _lib.moe_grouped_gemm_mxfp4_rows_size(M, w.desc_ref)
         if room:
-            with torch.cuda.stream(stream):  # memory of the stream that uses it
-                rows = torch.empty(room, dtype=u8, device=a_codes.device)
+            rows = _on(stream, torch.empty, room, dtype=u8, device=a_codes.device)
     if out is None:
-        out = torch.empty(M, N, dtype=torch.bfloat16, device=a_codes.device)
+        out = _on(stream, torch.empty, M, N, dtype=torch.bfloat16, device=a_codes.device)
     else:
         _want(out, "out", (M, N), torch.bfloat16, dev)
     if ws is None:
-        ws = torch.zeros(256, dtype=u8, device=a_codes.device)
+        ws = _on(stream, torch.zeros, 256, dtype=u8, device=a_codes.device)
     elif ws.get_device() != dev:
         raise ValueError(f"ws: need a workspace on cuda:{dev}, got {ws.device}")
     _check(_lib.moe_grouped_gemm_mxfp4_room(a_codes.data_ptr(), a_scales.data_ptr(), R, _ptr(row_idx), M, w.desc_ref,
@@ -476,7 +484,7 @@ def act_params(act: str = "silu", situ_alpha: float = 1.0, situ_beta: float = 1.
 def moe_act_and_mul(gate, up, perm_w=None, act: str = "silu", situ_alpha=1.0, situ_beta=1.0, out=None,
                     stream=None):
     M, I = gate.shape
-    out = out if out is not None else torch.empty_like(gate)
+    out = out if out is not None else _on(stream, torch.empty_like, gate)
     _check(_lib.moe_act_and_mul(_ptr(gate), _ptr(up), _ptr(perm_w), M, I,
                                 act_params(act, situ_alpha, situ_beta), _ptr(out), _stream(stream)),
            "moe_act_and_mul")
@@ -496,7 +504,7 @@ def moe_bias_act_and_mul(gate, up, cu_seqlens, bias_gate=None, bias_up=None, per
     """S4 with per-expert biases (fp32 [G,I]) and any activation, SWIGLUOAI included. gate/up
     bf16 or fp32 [M,I]; bf16 out [M,I]; rows past cu_seqlens[-1] come out zero."""
     M, I = gate.shape
-    out = out if out is not None else torch.empty(M, I, dtype=torch.bfloat16, device=gate.device)
+    out = out if out is not None else _on(stream, torch.empty, M, I, dtype=torch.bfloat16, device=gate.device)
     a = act_ex(act, situ_alpha, situ_beta, swiglu_alpha, swiglu_beta, swiglu_limit)
     _check(_lib.moe_bias_act_and_mul(_ptr(gate), _ptr(up), 1 if gate.dtype == torch.float32 else 0, _ptr(bias_gate),
                                      _ptr(bias_up), _ptr(cu_seqlens), cu_seqlens.numel(), _ptr(perm_w), M, I,
@@ -507,7 +515,7 @@ def moe_bias_act_and_mul(gate, up, cu_seqlens, bias_gate=None, bias_up=None, per
 def moe_combine(y_perm, inv_perm, topk_w=None, out=None, stream=None):
     T, k = inv_perm.shape
     H = y_perm.shape[1]
-    out = out if out is not None else torch.empty(T, H, dtype=torch.bfloat16, device=y_perm.device)
+    out = out if out is not None else _on(stream, torch.empty, T, H, dtype=torch.bfloat16, device=y_perm.device)
     _check(_lib.moe_combine(_ptr(y_perm), _ptr(inv_perm), _ptr(topk_w), T, k, H, _ptr(out),
                             _stream(stream)), "moe_combine")
     return out
@@ -516,10 +524,10 @@ def moe_combine(y_perm, inv_perm, topk_w=None, out=None, stream=None):
 def moe_quantize_nvfp4(x: torch.Tensor, deq: bool = True, stream=None):
     R, K = x.shape
     dev = x.device
-    codes = torch.empty(R, K // 2, dtype=torch.uint8, device=dev)
-    sb = torch.empty(R, K // 16, dtype=torch.uint8, device=dev)
-    s = torch.empty(R, dtype=torch.float32, device=dev)
-    d = torch.empty(R, K, dtype=torch.float16, device=dev) if deq else None
+    codes = _on(stream, torch.empty, R, K // 2, dtype=torch.uint8, device=dev)
+    sb = _on(stream, torch.empty, R, K // 16, dtype=torch.uint8, device=dev)
+    s = _on(stream, torch.empty, R, dtype=torch.float32, device=dev)
+    d = _on(stream, torch.empty, R, K, dtype=torch.float16, device=dev) if deq else None
     _check(_lib.moe_quantize_nvfp4(_ptr(x), 1 if x.dtype == torch.float32 else 0, R, K, _ptr(codes),
                                    _ptr(sb), _ptr(s), _ptr(d), _stream(stream)), "moe_quantize_nvfp4")
     return codes, sb, s, d
@@ -529,8 +537,8 @@ def moe_quantize_mxfp8(x: torch.Tensor, stream=None):
     """Dynamic MXFP8 quantisation of rows (bf16 or fp32 [R,K]): e4m3 codes [R,K] and e8m0
     scales [R,K/32]."""
     R, K = x.shape
-    codes = torch.empty(R, K, dtype=torch.uint8, device=x.device)
-    scales = torch.empty(R, K // 32, dtype=torch.uint8, device=x.device)
+    codes = _on(stream, torch.empty, R, K, dtype=torch.uint8, device=x.device)
+    scales = _on(stream, torch.empty, R, K // 32, dtype=torch.uint8, device=x.device)
     _check(_lib.moe_quantize_mxfp8(_ptr(x), 1 if x.dtype == torch.float32 else 0, R, K, _ptr(codes), _ptr(scales),
                                    _stream(stream)), "moe_quantize_mxfp8")
     return codes, scales
@@ -545,9 +553,9 @@ def moe_quantize_mxfp4(x: torch.Tensor, deq: bool = False, out=None, stream=None
     out = out or {}
     xt = _float_type(x, "x")
     stride = _want(x, "x", (R, K), xt, dev, False) or K
-    codes, _ = _output(out, "codes", x, (R, K // 2), torch.uint8, dev)
-    scales, _ = _output(out, "scales", x, (R, K // 32), torch.uint8, dev)
-    d = _output(out, "deq", x, (R, K), torch.bfloat16, dev)[0] if deq else None
+    codes, _ = _output(out, "codes", x, (R, K // 2), torch.uint8, dev, stream)
+    scales, _ = _output(out, "scales", x, (R, K // 32), torch.uint8, dev, stream)
+    d = _output(out, "deq", x, (R, K), torch.bfloat16, dev, stream)[0] if deq else None
     _check(_lib.moe_quantize_mxfp4(x.data_ptr(), xt is torch.float32, stride, R, K, codes.data_ptr(), scales.data_ptr(),
                                    _ptr(d), _launch_stream(dev, stream)), "moe_quantize_mxfp4")
     return codes, scales, d
@@ -596,6 +604,7 @@ class MoEForward:
         else:
             self.ws = forward_workspace(T_max, self.H, self.I, E, B, topk, w_gate.fmt, act_quant,
                                         w_gate.data.device)
+        self._made_on = torch.cuda.current_stream(self.ws.device) if self.ws.is_cuda else None
         self.args.routing = ROUTING[routing]
         self.routing_bias = routing_bias
         self.args.n_group, self.args.topk_group = n_group, topk_group
@@ -616,7 +625,12 @@ class MoEForward:
             self.args.stage_events = ctypes.cast(self._ev, ctypes.c_void_p)
         else:
             self.args.stage_events = None
-        out = out if out is not None else torch.empty(T, self.H, dtype=torch.bfloat16, device=x.device)
+        out = out if out is not None else _on(stream, torch.empty, T, self.H, dtype=torch.bfloat16, device=x.device)
+        if stream is not None:
+            if self._made_on is not None and not torch.cuda.is_current_stream_capturing():
+                self._made_on.synchronize()  # the workspace is free and zeroed before another stream has it
+                self._made_on = None
+            self.ws.record_stream(stream)  # and not handed out again before this call is done
         a = self.args
         a.x, a.router_logits = _ptr(x), _ptr(router_logits)
         a.T, a.H, a.I, a.E, a.B, a.topk = T, self.H, self.I, self.E, self.B, self.topk
