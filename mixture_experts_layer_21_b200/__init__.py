@@ -177,6 +177,23 @@ def _on(stream, make, *args, **kw) -> torch.Tensor:
         return make(*args, **kw)
 
 
+_error_words: dict[int, torch.Tensor] = {}
+
+
+def _error_word(dev: int) -> torch.Tensor:
+    """The error word of the calls on a device that get no workspace and need none but for it: one that
+    outlives them, so that moe_get_device_error() can read it. The first error stays until it is read."""
+    t = _error_words.get(dev)
+    if t is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("ws: the first call on a device needs one while a graph is captured")
+        with torch.cuda.device(dev):
+            t = torch.zeros(256, dtype=torch.uint8, device=f"cuda:{dev}")
+            torch.cuda.current_stream().synchronize()  # zero before a kernel on any stream
+        t = _error_words.setdefault(dev, t)
+    return t
+
+
 def _check(status: int, where: str) -> None:
     if status != MOE_OK:
         raise MoEError(status, where)
@@ -284,6 +301,7 @@ def moe_prepare_weights(w: Weight, stream=None) -> Weight:
     w.prepared = _on(stream, torch.empty, nbytes, dtype=torch.uint8, device=w.data.device)
     _check(_lib.moe_prepare_weights(ctypes.byref(w.desc), _ptr(w.prepared), nbytes, _stream(stream)),
            "moe_prepare_weights")
+    _error_word(w.prepared.get_device())  # made here, it is there when a product is captured
     return w
 
 
@@ -433,10 +451,11 @@ def moe_grouped_gemm(a: torch.Tensor, w: Weight, cu_seqlens: torch.Tensor, out=N
 def moe_grouped_gemm_nvfp4(a_codes: torch.Tensor, a_sb: torch.Tensor, a_s: torch.Tensor, w: Weight,
                            cu_seqlens: torch.Tensor, out=None, ws=None, stream=None) -> torch.Tensor:
     """Block-scaled grouped GEMM on NVFP4 activations (codes [M,K/2], e4m3 scales [M,K/16],
-    row scales [M]) and prepared NVFP4 weights; bf16 out [M,N]."""
+    row scales [M]) and prepared NVFP4 weights; bf16 out [M,N]. Without ``ws`` errors go to the device's
+    own error word, which moe_get_device_error() reads."""
     M = a_codes.shape[0]
     out = out if out is not None else _on(stream, torch.empty, M, w.N, dtype=torch.bfloat16, device=a_codes.device)
-    ws = ws if ws is not None else _on(stream, torch.zeros, 256, dtype=torch.uint8, device=a_codes.device)
+    ws = ws if ws is not None else _error_word(a_codes.get_device())
     _check(_lib.moe_grouped_gemm_nvfp4(_ptr(a_codes), _ptr(a_sb), _ptr(a_s), M, ctypes.byref(w.desc),
                                        _ptr(cu_seqlens), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
            "moe_grouped_gemm_nvfp4")
@@ -448,7 +467,9 @@ def moe_grouped_gemm_mxfp4(a_codes: torch.Tensor, a_scales: torch.Tensor, w: Wei
     """Block-scaled grouped GEMM on MXFP4 activations (codes [R,K/2], e8m0 scales [R,K/32]) and
     prepared MXFP4 weights. row_idx (int32 [M]): row r of the segments is row row_idx[r] of a (the
     permutation's perm_token), segments of many rows being gathered before the product into memory
-    allocated here; without it the R rows are in segment order. bf16 out [M,N]."""
+    allocated here; without it the R rows are in segment order. bf16 out [M,N]. What the kernel finds (an
+    index or a segment end out of range, a wait that ran out) is in ``ws`` (256 bytes, zeroed once), without
+    it in the device's own error word: moe_get_device_error(ws) or moe_get_device_error()."""
     R, dev, u8 = a_codes.shape[0], _launch_device(a_codes), torch.uint8
     K, N = w.K, w.N
     _want(a_codes, "a_codes", (R, K // 2), u8, dev)
@@ -468,7 +489,7 @@ def moe_grouped_gemm_mxfp4(a_codes: torch.Tensor, a_scales: torch.Tensor, w: Wei
     else:
         _want(out, "out", (M, N), torch.bfloat16, dev)
     if ws is None:
-        ws = _on(stream, torch.zeros, 256, dtype=u8, device=a_codes.device)
+        ws = _error_word(dev)
     elif ws.get_device() != dev:
         raise ValueError(f"ws: need a workspace on cuda:{dev}, got {ws.device}")
     _check(_lib.moe_grouped_gemm_mxfp4_room(a_codes.data_ptr(), a_scales.data_ptr(), R, _ptr(row_idx), M, w.desc_ref,
@@ -680,5 +701,9 @@ def moe_forward(x, router_logits, w_gate: Weight, w_up: Weight, w_down: Weight, 
     return out, layer
 
 
-def moe_get_device_error(ws: torch.Tensor, stream=None) -> int:
+def moe_get_device_error(ws: torch.Tensor | None = None, stream=None) -> int:
+    """Waits for the stream, then reads and clears the error word of a workspace; without one, that of the
+    calls on the current device that were given no workspace (moe_grouped_gemm_mxfp4 and _nvfp4)."""
+    if ws is None:
+        ws = _error_word(torch.cuda.current_device())
     return _lib.moe_get_device_error(_ptr(ws), _stream(stream))

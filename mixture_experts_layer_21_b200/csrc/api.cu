@@ -835,7 +835,9 @@ moe_status_t moe_get_device_error(void* ws, moe_stream_t stream) {
     DevError h{0, 0};
     if (cudaMemcpy(&h, ws, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
     if (h.code != 0) {
-        if (cudaMemset(ws, 0, sizeof(h)) != cudaSuccess) return MOE_ERR_CUDA;
+        // cleared before this returns: an error that the next call on any stream reports stays
+        if (cudaMemsetAsync(ws, 0, sizeof(h), S(stream)) != cudaSuccess) return MOE_ERR_CUDA;
+        if (cudaStreamSynchronize(S(stream)) != cudaSuccess) return MOE_ERR_CUDA;
         return static_cast<moe_status_t>(h.code);
     }
     return MOE_OK;
