@@ -125,8 +125,11 @@ struct Mxf4Cfg {
     static_assert(!PAIR || (BT % 32 == 0 && !GATHER), "pair MMA N: a multiple of 32; tokens by TMA");
     static_assert(STAGES >= 3 && SLOTS >= 2 && SMEM_BYTES <= kSmemLimit && SF_BASE + SLOTS * SF_SLOT <= 512, "MXFP4 GEMM config");
     static_assert(B_BYTES % 1024 == 0, "operand alignment");
-    // a warp that takes every n-th turn of a ring finds the turn of an entry before its own finished
-    static_assert((!GATHER || STAGES >= kGatherWarps) && kSfRing % SCALE_WARPS == 0 && kSfRing % COPIERS == 0, "turns of the rings");
+    // a warp that takes every n-th turn of a ring finds the turn of an entry before its own finished (a wait
+    // by parity a whole turn ahead of its barrier would pass at once); a copier that waits for the MMAs of
+    // SLOTS stages ago knows those of COPIERS stages before to be done, which has to be a turn of empty[]
+    static_assert((!GATHER || STAGES >= kGatherWarps) && kSfRing % SCALE_WARPS == 0 && kSfRing % COPIERS == 0 &&
+                      COPIERS <= STAGES, "turns of the rings");
 };
 
 MOE_DEV uint4 ld_shared16(uint32_t addr) {
@@ -182,11 +185,12 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
     // the MMA's width for a tile's rows, and the first row of this CTA's part of the token operand
     auto mma_n = [](int rows) { return PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; };
     auto part0 = [&](int rows) { return rank * (mma_n(rows) / 2); };
-    // A whole warp's wait, with acquire at this CTA's scope also where the other CTA of a pair arrives:
-    // what such an arrival announces is read by the tensor cores alone, and acquires at cluster scope
-    // made the pair's barriers alone take 396 us of the 14336 x 4096 case (8192 rows), against 93.
+    // A whole warp's wait; wait_peer where threads of the pair's other CTA arrive.
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_limit));
+    };
+    auto wait_peer = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait_relaxed(bar, parity, abort_flag, a.wait_limit));
     };
     auto commit = [](uint64_t* bar) {  // in both CTAs of a pair
         if (PAIR) mma_commit_pair(bar, 0x3);
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             uint32_t bph = 0, idesc = 0;
             bool ok = true, next_full = false, next_g = !GATHER;
             for (int L = first_tile; L < total && ok; L += tile_step, ++n) {
-                if (!wait(&ctl->tempty[b], bph ^ 1u)) {
+                if (!(PAIR ? wait_peer(&ctl->tempty[b], bph ^ 1u) : wait(&ctl->tempty[b], bph ^ 1u))) {
                     ok = false;
                     break;
                 }
@@ -364,11 +368,12 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
             for (int kb = 0; kb < KB; ++kb, ++it) {
                 if (C::COPIERS == 1 || it % C::COPIERS == mine) {
                     if (!wait(&mc->sf_ready[rg.i], rg.ph) ||
-                        (leader && ((PAIR && !wait(&mc->psf[rg.i], rg.ph)) ||
+                        (leader && ((PAIR && !wait_peer(&mc->psf[rg.i], rg.ph)) ||
                                     (it >= C::SLOTS && !wait(&ctl->empty[last.i], last.ph))))) {
                         ok = false;
                         break;
                     }
+                    if (PAIR && leader) fence_acquire_smem_cluster();
                     tc_fence_after();
                     const uint64_t src = ring0 + (uint64_t)(rg.i * (C::SF_ENTRY >> 4));
                     const uint32_t sfa = tmem_base + (uint32_t)(C::SF_BASE + sl.i * C::SF_SLOT), sfb = sfa + 8;
@@ -379,6 +384,7 @@ __global__ void __launch_bounds__(Mxf4Cfg<BT, GATHER, PAIR>::THREADS, 1)
                     };
                     if (elect_one()) {
                         if (!leader) {
+                            fence_release_smem_cluster();  // both sides' blocks, which this warp has waited for
                             mbar_arrive_remote(mapa_shared(smem_u32(&mc->psf[rg.i]), 0));
                         } else {
 #pragma unroll
