@@ -152,6 +152,7 @@ moe_status_t moe_route_topk_grouped(const float* logits, const float* bias, int 
  * 0, so that ids stay valid and distinct for moe_permute. A row without a live expert gets
  * weight 0 throughout. Softmax gives +inf logits equal shares of 1. Decisions are those of
  * 64-bit arithmetic: 32-bit scores decide only where they differ by more than their error.
+ * Weights are formed in 64 bits and rounded once.
  *   logits fp32 (in_is_bf16 = 0) or bf16 (1) [T,E], rows row_stride elements apart (>= E).
  *   topk_ids int32 / topk_w fp32 [T,topk] out, dense.
  * E % n_group, 1 <= topk_group <= n_group, 1 <= topk <= topk_group*E/n_group and a finite

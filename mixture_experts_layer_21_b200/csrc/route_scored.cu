@@ -11,7 +11,8 @@
 // The decisions are those of fp64. The scores are computed in fp32 first, with a bound on their
 // error, and where every comparison that decides is wider than it (but for a token in some
 // hundreds), that is the answer; else fp64 decides among the candidates that are too close. In fp64
-// throughout 16384 tokens x 256 experts in 8 groups took 158 us.
+// throughout 16384 tokens x 256 experts in 8 groups took 158 us. The weights of the chosen are formed in
+// fp64 and rounded once.
 #include "internal.h"
 
 namespace moe {
@@ -26,7 +27,21 @@ MOE_DEV float load_logit(const void* row, int e) {
     return static_cast<const float*>(row)[e];
 }
 
+MOE_DEV float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // ----------------------------------------------------------------- fp64
+// 1 / d for d > 0: fp32's reciprocal, within 2^-23, and one Newton step, r (2 - d r), which squares that:
+// within 2^-45 (a division takes three times the instructions). Divided where fp32 does not hold d or 1 / d.
+MOE_DEV double recip64(double d) {
+    if (!(d > 0x1p-100 && d < 0x1p100)) return 1.0 / d;
+    const double r = (double)rcp_approx((float)d);
+    return fma(r, fma(-d, r, 1.0), r);
+}
+
 // What one warp needs of a token in fp64, from the logits in memory (in the cache by then). The
 // functions are called for few tokens and stay out of line: the registers of their loops would cost
 // the other tokens occupancy.
@@ -44,10 +59,16 @@ struct Token64 {
         return isnan(x) ? -INFINITY : x;
     }
     // the score, softmax's without its denominator: the largest logit's is 1 whether it is finite or +inf
+    MOE_DEV double expo(float l) const {
+        return exp(a.scoring == MOE_SCORE_SIGMOID ? -(double)l : l == mx ? 0.0 : (double)l - (double)mx);
+    }
     MOE_DEV double part(float l) const {
-        const double x = a.scoring == MOE_SCORE_SIGMOID ? -(double)l : l == mx ? 0.0 : (double)l - (double)mx;
-        const double z = exp(x);
+        const double z = expo(l);
         return l == -INFINITY ? 0.0 : a.scoring == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + z) : z;
+    }
+    MOE_DEV double weight(float l) const {  // the score for the output, within 2^-44
+        const double z = expo(l);
+        return l == -INFINITY ? 0.0 : a.scoring == MOE_SCORE_SIGMOID ? recip64(1.0 + z) : z * recip64(norm);
     }
     MOE_DEV void set_norm(double sum) {  // sum: this lane's
 #pragma unroll
@@ -149,6 +170,34 @@ __device__ __noinline__ int order64(const moe_route_args_t& a, int t, float mx, 
     return best;
 }
 
+// The sum of a softmax row's numerators.
+template <bool BF16>
+__device__ __noinline__ double norm64(const moe_route_args_t& a, int t, float mx) {
+    Token64<BF16> k(a, t, mx);
+    double sum = 0.0;
+#pragma unroll 4
+    for (int e = lane_id(); e < a.E; e += 32) sum += k.part(k.logit(e));
+    k.set_norm(sum);
+    return k.norm;
+}
+
+// Writes the choice, lane j's the j-th, with its weights.
+template <bool BF16>
+__device__ __forceinline__ void write64(const Token64<BF16>& k, int t, int my_id) {
+    const moe_route_args_t& a = k.a;
+    const int lane = lane_id();
+    double w = lane < a.topk ? k.weight(k.logit(my_id)) : 0.0;
+    if (a.renormalize) {
+        double tot = w;
+        for (int off = 1; off < a.topk; off <<= 1) tot += __shfl_xor_sync(0xffffffffu, tot, off);  // 0 from topk on
+        w = tot > 0.0 ? w * recip64(tot) : 0.0;
+    }
+    if (lane < a.topk) {
+        a.topk_ids[(size_t)t * a.topk + lane] = my_id;
+        a.topk_w[(size_t)t * a.topk + lane] = (float)((double)a.routed_scaling_factor * w);
+    }
+}
+
 // A whole token.
 template <bool BF16>
 __device__ __noinline__ void route64(const moe_route_args_t& a, int t, double* c) {
@@ -196,17 +245,7 @@ __device__ __noinline__ void route64(const moe_route_args_t& a, int t, double* c
         if ((bid & 31) == lane) c[bid] = gone;
         __syncwarp();
     }
-    double w = lane < a.topk ? k.part(k.logit(my_id)) / k.norm : 0.0;
-    if (a.renormalize) {
-        double tot = w;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, off);
-        w = tot > 0.0 ? w / tot : 0.0;
-    }
-    if (lane < a.topk) {
-        a.topk_ids[(size_t)t * a.topk + lane] = my_id;
-        a.topk_w[(size_t)t * a.topk + lane] = (float)((double)a.routed_scaling_factor * w);
-    }
+    write64(k, t, my_id);
 }
 
 // ----------------------------------------------------------------- fp32
@@ -242,11 +281,6 @@ MOE_DEV float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-MOE_DEV float rcp_approx(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 
 // What the host works out once for the launch.
 struct RoutePlan {
@@ -256,10 +290,10 @@ struct RoutePlan {
     int lanes, shift; // GROUPS: a group is an aligned run of `lanes` = 2^shift lanes; lanes = 0: it is not
 };
 
-// One token, in fp32 where that decides. False where it cannot (infinite logits, more than 32
+// One token, decided in fp32 where that decides. False where it cannot (infinite logits, more than 32
 // candidates within the error of each other); nothing is written then. What bounds it is the number
-// of instructions (1046 a token with 256 experts in 8 groups, 27 us for 16384 tokens; at 1260 30 us, at
-// 1600 36).
+// of instructions (with 256 experts in 8 groups 1046 a token took 27 us for 16384 tokens, 1260 30 us, 1600
+// 36; the weights in fp64 brought 27.0 to 28.7, with fp64 divisions 29.3).
 //
 // Error of the scores that rank. Sigmoid: the exponential's argument -l log2(e) rounds twice, 2^-23 |l|
 // relative to the exponential e, whose approximation is within 2^-22; e / (1 + e)^2 <= 1/4 and |l| e / (1 + e)^2
@@ -267,12 +301,12 @@ struct RoutePlan {
 // Softmax: the argument (l - max) log2(e) rounds three times; |x| e^-|x| <= 0.37, so a term is within 2^-22 of
 // the largest and, weighted by the terms, whose mean |x| is at most ln 1024 < 7, the sum within 13 * 2^-23,
 // and 37 * 2^-24 for its additions, a chain of 32 in a lane and 5 across: s is within 2^-18 of itself and
-// 2^-22 of the largest. (Raw softmax weights take the exact exponential for their sum.) Adding the bias
-// rounds once more, 2^-24 |c|. Two values compare as their exact ones do if they differ by more than the
-// sum of both bounds; the slacks below are twice that. Logits compare exactly.
+// 2^-22 of the largest. Adding the bias rounds once more, 2^-24 |c|. Two values compare as their exact ones
+// do if they differ by more than the sum of both bounds; the slacks below are twice that. Logits compare
+// exactly.
 template <int EPL, bool BF16, bool GROUPS>
 __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, const float (&l)[EPL], int t,
-                           const void* row, double* c64) {
+                           double* c64) {
     constexpr float LOG2E = 1.44269504f;
     const int lane = lane_id(), E = a.E;
     const bool softmax = a.scoring == MOE_SCORE_SOFTMAX;
@@ -284,18 +318,29 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
         mx = key_value(__reduce_max_sync(0xffffffffu, order_key(m)));
         if (!(mx < INFINITY && mx > -INFINITY)) return false;  // +inf logits, or no live expert
     }
-    // scores of every expert, where the selection, the groups or the raw softmax weights need them
+    // raw softmax weights need the denominator in fp64 (renormalised, it cancels)
+    Token64<BF16> k(a, t, mx);
+    if (softmax && !a.renormalize) {
+        if (EPL <= 8) {
+            double sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) sum += k.part(l[i]);
+            k.set_norm(sum);
+        } else {
+            k.norm = norm64<BF16>(a, t, mx);
+        }
+    }
+    // scores of every expert, where the selection or the groups need them
     const bool top2 = GROUPS && a.group_score == MOE_GROUP_TOP2;
-    const bool raw = softmax && !a.renormalize;
     auto approx = [&](float x) {  // softmax: without its denominator; 0 where masked
         return softmax ? exp2_approx((x - mx) * LOG2E) : rcp_approx(1.0f + exp2_approx(x * -LOG2E));
     };
-    if (a.bias || raw || top2) {
+    if (a.bias || top2) {
         if (softmax) {
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
-                s[i] = raw ? expf(l[i] - mx) : approx(l[i]);
+                s[i] = approx(l[i]);
                 sum += s[i];
             }
 #pragma unroll
@@ -477,28 +522,7 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
             if (keys[my_from * EPL + i] == my_key && n-- == 0) my_id = my_from * EPL + i;
     }
     if (close) my_id = order64<BF16>(a, t, mx, my_id, count);
-    const bool mine = lane < a.topk;
-    float w = 0.0f, arg = 0.0f;
-    if (mine) {
-        // the chosen logit once more (from the cache): its score with exact functions
-        const float x = load_logit<BF16>(row, my_id);
-        const bool off = isnan(x) || x == -INFINITY;
-        arg = off ? 0.0f : softmax ? x - mx : x;
-        w = off ? 0.0f : softmax ? expf(arg) * (a.renormalize ? 1.0f : inv) : 1.0f / (1.0f + expf(-arg));
-    }
-    // far from the largest (or from 0) fp32's exponential leaves its normal range
-    if (__any_sync(0xffffffffu, arg < -80.0f)) return false;
-    if (a.renormalize) {
-        float tot = w;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, off);
-        if (!(tot > 0.0f)) return false;
-        w /= tot;
-    }
-    if (mine) {
-        a.topk_ids[(size_t)t * a.topk + lane] = my_id;
-        a.topk_w[(size_t)t * a.topk + lane] = a.routed_scaling_factor * w;
-    }
+    write64(k, t, my_id);
     return true;
 }
 
@@ -544,7 +568,7 @@ __global__ void __launch_bounds__(128, EPL <= 8 ? 8 : 4) route_scored_kernel(con
         float l[EPL];
         load_logits<EPL, BF16>(a, row, plan.wide, l);
         double* c64 = warps_c64 + warp_id() * (32 * EPL);
-        if (!route_fast<EPL, BF16, GROUPS>(a, plan, l, t, row, c64)) route64<BF16>(a, t, c64);
+        if (!route_fast<EPL, BF16, GROUPS>(a, plan, l, t, c64)) route64<BF16>(a, t, c64);
     }
     pdl_launch();
 }
