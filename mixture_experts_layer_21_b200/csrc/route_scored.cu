@@ -13,6 +13,8 @@
 // hundreds), that is the answer; else fp64 decides among the candidates that are too close. In fp64
 // throughout 16384 tokens x 256 experts in 8 groups took 158 us. The weights of the chosen are formed in
 // fp64 and rounded once.
+#include <cfloat>
+
 #include "internal.h"
 
 namespace moe {
@@ -302,8 +304,10 @@ struct RoutePlan {
 // the largest and, weighted by the terms, whose mean |x| is at most ln 1024 < 7, the sum within 13 * 2^-23,
 // and 37 * 2^-24 for its additions, a chain of 32 in a lane and 5 across: s is within 2^-18 of itself and
 // 2^-22 of the largest. Adding the bias rounds once more, 2^-24 |c|. Two values compare as their exact ones
-// do if they differ by more than the sum of both bounds; the slacks below are twice that. Logits compare
-// exactly.
+// do if they differ by more than the sum of both bounds; the slacks below are twice that. They take the
+// magnitudes of the values compared, not those of other experts: one that a bias of -1e9 switches off does
+// not make the others close (with slacks from the largest |bias| it sent every token to fp64). Logits and
+// infinite values compare exactly.
 template <int EPL, bool BF16, bool GROUPS>
 __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, const float (&l)[EPL], int t,
                            double* c64) {
@@ -375,7 +379,7 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
         }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            bmax = fmaxf(bmax, fabsf(b[i]));
+            if (softmax) bmax = fmaxf(bmax, fabsf(b[i]));
             const float c = s[i] + b[i];  // not -0: s is not
             key[i] = order_bits(l[i] > -INFINITY && c > -INFINITY ? c : -INFINITY);  // NaN as -inf
         }
@@ -388,25 +392,18 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
         for (int i = 0; i < EPL; ++i)
             if (i >= live) key[i] = 0u;
     }
-    if (a.bias) {
-        bmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
-        if (bmax == INFINITY) {  // the largest finite one: an infinite sum has no error
-            bmax = 0.0f;
-            for (int i = 0; i < live; ++i) {
-                const float f = fabsf(__ldg(a.bias + lane * EPL + i));
-                if (f < INFINITY) bmax = fmaxf(bmax, f);
-            }
-            bmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
-        }
-    }
+    if (a.bias && softmax) bmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
     // A group's score from the two largest keys of c (of the logits without a bias, whose order is that of
-    // s; where the best expert ranks the group, they are its score).
+    // s; where the best expert ranks the group, they are its score); mag: the sum of the magnitudes in it.
     constexpr uint32_t MASKED = 0x007fffffu;  // order_key(-INFINITY)
-    auto score = [&](uint32_t a1, uint32_t a2) {
+    auto score = [&](uint32_t a1, uint32_t a2, float& mag) {
         const float best = a1 ? key_value(a1) : -INFINITY;
-        if (!top2) return best;
+        mag = fabsf(best);
+        if (!top2 || a1 <= MASKED) return best;
         auto part = [&](float x) { return a.bias ? x : approx(x) * inv; };
-        return a1 <= MASKED ? -INFINITY : a2 <= MASKED ? part(best) : part(best) + part(key_value(a2));
+        const float c1 = part(best), c2 = a2 <= MASKED ? 0.0f : part(key_value(a2));
+        mag = fabsf(c1) + fabsf(c2);
+        return c1 + c2;
     };
     auto merge = [](uint32_t& a1, uint32_t& a2, uint32_t b1, uint32_t b2) {
         a2 = max(min(a1, b1), max(a2, b2));
@@ -446,7 +443,9 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
             const uint32_t b1 = __shfl_xor_sync(0xffffffffu, a1, off), b2 = __shfl_xor_sync(0xffffffffu, a2, off);
             merge(a1, a2, b1, b2);
         }
-        const float my = __shfl_sync(0xffffffffu, score(a1, a2), min(lane * lanes, 31));
+        const int src = min(lane * lanes, 31);
+        float mag;
+        const float own = score(a1, a2, mag), my = __shfl_sync(0xffffffffu, own, src);
         int rank = 0;  // how many groups come before this lane's
         for (int h = 0; h < a.n_group; ++h) {
             const float o = __shfl_sync(0xffffffffu, my, h);
@@ -454,11 +453,13 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
         }
         const bool is = lane < a.n_group, kept = is && rank < a.topk_group;
         uint32_t keep = __ballot_sync(0xffffffffu, kept);
-        if (top2 || a.bias) {  // the lowest kept against the highest dropped score: up to four c
-            const float lo = key_value(__reduce_min_sync(0xffffffffu, kept ? order_key(my) : 0xffffffffu));
-            const float hi = key_value(__reduce_max_sync(0xffffffffu, is && !kept ? order_key(my) : 0u));
-            const float slack = (softmax ? 0x1p-17f * 2.0f + 0x1p-19f : 0x1p-20f * 4.0f) + 0x1p-22f * 4.0f * (1.0f + bmax);
-            if (!(lo - hi > slack)) keep = groups64<BF16>(a, t, mx, c64);
+        if (top2 || a.bias) {  // the lowest kept score's lower end against the highest dropped one's upper end
+            // a score's slack: of its s, up to two of them (softmax's sum to at most 1), and of the rounding of
+            // its c and of their sum
+            const float e = __shfl_sync(0xffffffffu, (softmax ? 0x1p-17f + 0x1p-20f : 0x1p-19f) + 0x1p-22f * fminf(mag, FLT_MAX), src);
+            const float lo = key_value(__reduce_min_sync(0xffffffffu, kept ? order_key(my - e) : 0xffffffffu));
+            const float hi = key_value(__reduce_max_sync(0xffffffffu, is && !kept ? order_key(my + e) : 0u));
+            if (!(lo > hi)) keep = groups64<BF16>(a, t, mx, c64);
         }
         if (plan.lanes) {
             const int g = lane >> plan.shift;
@@ -480,12 +481,13 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
     // times (the kept groups hold as many experts); lane j keeps the j-th. With a bias the candidates go
     // on to those within the error of the last chosen, and where two neighbours are that close, fp64
     // orders the candidates: any other expert is below topk of them.
-    // The slack of two c: s_i + s_j <= |c_i| + |c_j| + 2 bmax for softmax; sigmoid's s are at most 1.
-    const float slack0 = softmax ? 0x1p-16f * bmax + 0x1p-20f * inv : 0x1p-19f + 0x1p-21f * (1.0f + bmax);
-    const float slack1 = softmax ? 0x1p-17f + 0x1p-22f : 0.0f;
-    // masked experts (c = -inf, no slack) are behind every live one, in order of id
+    // The slack of two c. Softmax: s_i + s_j <= |c_i| + |c_j| + 2 bmax and at most twice the largest, inv;
+    // sigmoid's s are at most 1. Masked experts (c = -inf) are behind every live one, in order of id.
+    const bool by_c = softmax && bmax < inv;
+    const float slack0 = softmax ? 0x1p-16f * fminf(bmax, inv) + 0x1p-20f * inv : 0x1p-19f;
+    const float slack1 = by_c ? 0x1p-17f + 0x1p-22f : 0x1p-22f;
     auto near = [&](float hi, float c) {
-        return c > -INFINITY && !(hi - c > slack0 + slack1 * (fabsf(hi) + fabsf(c)));
+        return fabsf(c) < INFINITY && !(hi - c > slack0 + slack1 * fminf(fabsf(hi) + fabsf(c), FLT_MAX));
     };
     uint32_t my_key = 0u, last = 0u;
     int my_from = 0, count = 0;
