@@ -433,8 +433,8 @@ moe_status_t moe_quantize_mxfp4(const void* in, int in_is_f32, int64_t in_stride
  *   w       MXFP4 weights prepared by moe_prepare_weights (else NOT_PREPARED); other formats:
  *           UNSUPPORTED.
  *   out bf16 [M_alloc, N], N % 8 == 0; cu_seqlens int32 [G] on device; G <= 1024.
- *   ws: at least 256 bytes (the error word). The first call on a device sets kernel attributes:
- *   make it before any stream capture.
+ *   ws: at least 256 bytes (the error word). The first call on a device, whatever its sizes, sets the
+ *   attributes of every kernel: make it before any stream capture.
  *   rows: NULL. (It took memory for gathered rows without its size; a pointer is refused with
  *   MOE_ERR_INVALID_ARG.)
  * moe_grouped_gemm_mxfp4_room is the same call with memory for gathered rows:

@@ -645,17 +645,53 @@ bool make_map_codes(CUtensorMap* m, const void* ptr, uint64_t bytes, uint64_t N,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int kPairTile = 192, kOrderedTile = 64;  // kOrderedTile: from here on rows are gathered first
+
 template <int BT, bool GATHER, bool PAIR>
-cudaError_t run_mxf4(const CUtensorMap& ta, const CUtensorMap& tw, Mxf4Args a, cudaStream_t st, bool pdl) {
+cudaError_t set_attributes() {
+    return cudaFuncSetAttribute(grouped_gemm_mxf4_kernel<BT, GATHER, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Mxf4Cfg<BT, GATHER, PAIR>::SMEM_BYTES);
+}
+template <int BT>
+cudaError_t set_attributes_of_tile() {
+    const cudaError_t e = set_attributes<BT, false, false>();
+    return e == cudaSuccess ? set_attributes<BT, true, false>() : e;
+}
+
+// What the first call on a device sets up, for every tile: a later call of another size has nothing left to
+// do before its launches, in a stream capture too. pairs: how many CTA pairs run at once, 0 where none can.
+struct DeviceSetup {
+    std::once_flag once;
+    cudaError_t status = cudaSuccess;
+    int pairs = 0;
+};
+cudaError_t device_setup(int* pairs) {
+    static DeviceSetup setups[64];
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    DeviceSetup& d = setups[dev];
+    std::call_once(d.once, [&d] {
+        cudaError_t (*const all[])() = {set_attributes_of_tile<16>, set_attributes_of_tile<32>, set_attributes_of_tile<64>,
+                                        set_attributes_of_tile<128>, set_attributes<kPairTile, false, true>};
+        for (auto set : all)
+            if (d.status == cudaSuccess) d.status = set();
+        if (d.status != cudaSuccess) return;
+        using C = Mxf4Cfg<kPairTile, false, true>;
+        int cache[64] = {0};
+        d.pairs = max_pairs_once(grouped_gemm_mxf4_kernel<kPairTile, false, true>, C::SMEM_BYTES, C::THREADS, cache);
+        if (d.pairs < 1) cudaGetLastError();  // no error of the call's: it takes one-SM tiles
+    });
+    *pairs = d.pairs;
+    return d.status;
+}
+
+template <int BT, bool GATHER, bool PAIR>
+cudaError_t run_mxf4(const CUtensorMap& ta, const CUtensorMap& tw, Mxf4Args a, int maxp, cudaStream_t st, bool pdl) {
     using C = Mxf4Cfg<BT, GATHER, PAIR>;
     auto kern = grouped_gemm_mxf4_kernel<BT, GATHER, PAIR>;
-    static int done[64] = {0};
-    cudaError_t e = set_smem_once(kern, C::SMEM_BYTES, done);
-    if (e != cudaSuccess) return e;
     if (PAIR) {
-        static int pairs_cache[64] = {0};
-        const int maxp = max_pairs_once(kern, C::SMEM_BYTES, C::THREADS, pairs_cache);
-        if (maxp < 1) return cudaErrorInvalidConfiguration;
         a.NT = (a.NT1 + 1) / 2;
         const long long tiles = ((long long)(a.M_alloc + BT - 1) / BT + a.G) * a.NT;
         const int pairs = (int)std::min<long long>(maxp, tiles);
@@ -668,12 +704,12 @@ cudaError_t run_mxf4(const CUtensorMap& ta, const CUtensorMap& tw, Mxf4Args a, c
 }
 
 template <int BT, bool PAIR = false>
-cudaError_t run_mxf4_bt(const Mxf4Problem& p, const CUtensorMap& tw, const Mxf4Args& a, cudaStream_t st, bool pdl) {
+cudaError_t run_mxf4_bt(const Mxf4Problem& p, const CUtensorMap& tw, const Mxf4Args& a, int maxp, cudaStream_t st, bool pdl) {
     CUtensorMap ta;
     if (!make_map_u8(&ta, p.a_codes, (uint64_t)p.K / 2, p.a_rows, p.K / 2, kStageK / 2, PAIR ? BT / 2 : BT,
                      CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    return p.row_idx ? run_mxf4<BT, !PAIR, PAIR>(ta, tw, a, st, pdl) : run_mxf4<BT, false, PAIR>(ta, tw, a, st, pdl);
+    return p.row_idx ? run_mxf4<BT, !PAIR, PAIR>(ta, tw, a, maxp, st, pdl) : run_mxf4<BT, false, PAIR>(ta, tw, a, maxp, st, pdl);
 }
 
 // The rows that row_idx names, copied into segment order, a warp to a row: a product in tiles of 64 tokens
@@ -710,8 +746,6 @@ __global__ void __launch_bounds__(256) gather_mxfp4_rows_kernel(const uint8_t* _
     pdl_launch();
 }
 
-constexpr int kPairTile = 192, kOrderedTile = 64;  // kOrderedTile: from here on rows are gathered first
-
 }  // namespace
 
 // Token tile: a tile costs a stage per 256 K whatever its width, so it should hold a whole segment;
@@ -741,7 +775,10 @@ size_t gemm_mxf4_rows_bytes(int tile, int K, int M_alloc) {
 
 cudaError_t launch_gemm_mxf4(const Mxf4Problem& problem, cudaStream_t st, bool pdl) {
     Mxf4Problem p = problem;
-    const int bt = p.tile;
+    int maxp = 0;
+    const cudaError_t ready = device_setup(&maxp);
+    if (ready != cudaSuccess) return ready;
+    const int bt = p.tile == kPairTile && maxp < 1 ? 128 : p.tile;  // no clusters of two here: one SM a tile
     if (bt >= kOrderedTile && p.row_idx && p.rows) {
         uint8_t* codes = static_cast<uint8_t*>(p.rows);
         uint8_t* scales = codes + (size_t)p.M_alloc * (p.K / 2);
@@ -776,11 +813,11 @@ cudaError_t launch_gemm_mxf4(const Mxf4Problem& problem, cudaStream_t st, bool p
     l2_policies(&a.l2_w, &a.l2_t);
     CUtensorMap tw;
     if (!make_map_codes(&tw, p.kdata, (uint64_t)Kp / 2, p.N, p.G)) return cudaErrorInvalidValue;
-    if (bt == kPairTile) return run_mxf4_bt<kPairTile, true>(p, tw, a, st, pdl);
-    if (bt == 16) return run_mxf4_bt<16>(p, tw, a, st, pdl);
-    if (bt == 32) return run_mxf4_bt<32>(p, tw, a, st, pdl);
-    if (bt == 64) return run_mxf4_bt<64>(p, tw, a, st, pdl);
-    return run_mxf4_bt<128>(p, tw, a, st, pdl);
+    if (bt == kPairTile) return run_mxf4_bt<kPairTile, true>(p, tw, a, maxp, st, pdl);
+    if (bt == 16) return run_mxf4_bt<16>(p, tw, a, maxp, st, pdl);
+    if (bt == 32) return run_mxf4_bt<32>(p, tw, a, maxp, st, pdl);
+    if (bt == 64) return run_mxf4_bt<64>(p, tw, a, maxp, st, pdl);
+    return run_mxf4_bt<128>(p, tw, a, maxp, st, pdl);
 }
 
 }  // namespace moe
