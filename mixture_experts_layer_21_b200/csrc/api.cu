@@ -43,6 +43,8 @@ namespace {
 
 inline cudaStream_t S(moe_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// An int32 array or an error word, which kernels add to: at an odd address that would fault.
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 inline size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 
@@ -286,6 +288,7 @@ moe_status_t moe_grouped_gemm_mxfp4_room(const uint8_t* a_codes, const uint8_t* 
     if (a_rows < 1 || (!row_idx && a_rows < M_alloc)) return MOE_ERR_INVALID_ARG;
     if (!a_codes || !a_scales || !cu_seqlens || !out || !ws) return MOE_ERR_INVALID_ARG;
     if (!aligned16(a_codes) || !aligned16(out) || !aligned16(rows) || w->N % 8) return MOE_ERR_ALIGNMENT;
+    if (!aligned4(cu_seqlens) || !aligned4(row_idx) || !aligned4(ws)) return MOE_ERR_ALIGNMENT;
     if (ws_bytes < kErrBytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
     // the tile is chosen once: the room is checked for the launch that uses it
     const int tile = gemm_mxf4_tile(w->G, w->N, M_alloc, !row_idx || rows);
@@ -323,6 +326,7 @@ moe_status_t moe_permute(const int32_t* topk_ids, const float* topk_w, int T, in
         if (H % 8 || !aligned16(x) || !aligned16(x_perm)) return MOE_ERR_ALIGNMENT;
     }
     if (T > 0 && (!topk_ids || !perm_token || !perm_w || !inv_perm)) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(ws)) return MOE_ERR_ALIGNMENT;
     char* w = static_cast<char*>(ws);
     cudaStream_t st = S(stream);
     cudaError_t e = launch_permute(topk_ids, topk_w, T, topk, E, B, replica_src, cu_seqlens, perm_token, perm_w,
@@ -349,6 +353,8 @@ moe_status_t moe_grouped_gemm(const void* a, int M_alloc, const moe_weight_t* w,
     if (M_alloc == 0) return MOE_OK;
     if (!a || !cu_seqlens || !out || !ws) return MOE_ERR_INVALID_ARG;
     if (!aligned16(a) || !aligned16(out) || w->N % 8) return MOE_ERR_ALIGNMENT;
+    // FP4 weights: the staged rows lie in it
+    if (!aligned4(cu_seqlens) || !(w->fmt == MOE_W_BF16 ? aligned4(ws) : aligned16(ws))) return MOE_ERR_ALIGNMENT;
     if (ws_bytes < moe_grouped_gemm_workspace_size(M_alloc, w)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     cudaStream_t st = S(stream);
     char* wsb = static_cast<char*>(ws);
@@ -420,6 +426,7 @@ moe_status_t moe_grouped_gemm_nvfp4(const uint8_t* a_codes, const uint8_t* a_sb,
     if (M_alloc == 0) return MOE_OK;
     if (!a_codes || !a_sb || !a_s || !cu_seqlens || !out || !ws) return MOE_ERR_INVALID_ARG;
     if (!aligned16(a_codes) || !aligned16(a_sb) || !aligned16(out) || w->N % 8) return MOE_ERR_ALIGNMENT;
+    if (!aligned4(cu_seqlens) || !aligned4(ws)) return MOE_ERR_ALIGNMENT;
     if (ws_bytes < kErrBytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
     GemmProblem p{};
     p.x = a_codes;
@@ -568,6 +575,7 @@ moe_status_t moe_forward(const moe_forward_args_t* p, void* ws, size_t ws_bytes,
     if (!ws) return MOE_ERR_INVALID_ARG;
     const FwdWs L = fwd_layout(p->T_max, H, I, E, B, k, fmt, p->act_quant);
     if (ws_bytes < L.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;
     if (T == 0) return MOE_OK;
     if (!p->x || (!p->router_logits && p->routing != 2) || !p->out) return MOE_ERR_INVALID_ARG;
     if (!aligned16(p->x) || !aligned16(p->out) || !aligned16(ws)) return MOE_ERR_ALIGNMENT;
