@@ -106,3 +106,25 @@ def test_fp4_weights_on_bf16_rows_and_on_nvfp4_rows(ends, fmt):
         got = call(torch.from_numpy(given).int().cuda(), ws)
         assert m.moe_get_device_error(ws) == _expected_error(given, 60)
         assert torch.equal(got, want) and not bool(got[int(clamped[-1]):].any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tile", ["16", "64", "pairs"])
+def test_many_segments_with_falls(tile, monkeypatch):
+    """More segments than a warp has lanes, ends that fall inside and across its chunks of 32."""
+    monkeypatch.setenv("MOE_GEMM_PAIRS", "1" if tile == "pairs" else "0")
+    monkeypatch.setenv("MOE_TOKEN_TILE", "16" if tile == "pairs" else tile)
+    lens = [5, 0, 7] * 26
+    case = list(_case(lens, 72, 64, False, seed=6))
+    M = case[-1]
+    given = np.cumsum(lens)
+    given[[3, 31, 32, 40, 63, 64, 76]] = [0, 2, 200, 1, -4, 30, M + 9]
+    ac, asc, wc, wsc, M = case[0], case[1], case[2], case[3], case[7]
+    w = m.moe_prepare_weights(m.Weight("mxfp4", wc.cuda(), wsc.cuda()))
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    got = m.moe_grouped_gemm_mxfp4(ac.cuda(), asc.cuda(), w, torch.from_numpy(given).int().cuda(), ws=ws)
+    torch.cuda.synchronize()
+    assert m.moe_get_device_error(ws) == DEVICE
+    case[6] = torch.from_numpy(_clamped(given, M)).int()
+    ref, slack = _reference(tuple(case))
+    assert np.all(np.abs(got.double().cpu().numpy() - ref) <= slack + (np.abs(ref) + slack) * 2.0 ** -8)
