@@ -429,7 +429,7 @@ moe_status_t moe_quantize_mxfp4(const void* in, int in_is_f32, int64_t in_stride
  *   a_codes uint8 [a_rows, K/2];  a_scales uint8 [a_rows, K/32] — the outputs of
  *           moe_quantize_mxfp4 or moe_add_rmsnorm.
  *   row_idx int32 [M_alloc] or NULL (a_rows >= M_alloc): the permutation's perm_token, so that
- *           token rows quantised once are gathered by the GEMM itself.
+ *           token rows are quantised once, before it; the call gathers them (see rows).
  *   w       MXFP4 weights prepared by moe_prepare_weights (else NOT_PREPARED); other formats:
  *           UNSUPPORTED.
  *   out bf16 [M_alloc, N], N % 8 == 0; cu_seqlens int32 [G] on device; G <= 1024.

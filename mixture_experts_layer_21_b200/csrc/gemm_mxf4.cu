@@ -714,9 +714,9 @@ cudaError_t run_mxf4_bt(const Mxf4Problem& p, const CUtensorMap& tw, const Mxf4A
 
 // The rows that row_idx names, copied into segment order, a warp to a row: a product in tiles of 64 tokens
 // and more gains more from rows in order than the copy takes, which is about 3 us (8192 rows x 4096 into
-// 14336 on pairs: 250 us when gathering in the product took 289. 128 experts x 2880 x 2880 with 64 rows
-// each 121 and 140, with 32 rows 102 and 107, with 8 rows 98 and 95). Rows behind the segments are left
-// out: their row_idx may be anything.
+// 14336: 239 us on pairs, 266 in 128-token tiles of one SM, 368 when those gather. 128 experts x 2880 x 2880
+// with 64 rows each 106 and 138, with 32 rows 103 and 102, with 8 rows 100 and 94). Rows behind the
+// segments are left out: their row_idx may be anything.
 __global__ void __launch_bounds__(256) gather_mxfp4_rows_kernel(const uint8_t* __restrict__ codes,
                                                                 const uint8_t* __restrict__ scales, int a_rows,
                                                                 const int32_t* __restrict__ row_idx,
@@ -750,8 +750,10 @@ __global__ void __launch_bounds__(256) gather_mxfp4_rows_kernel(const uint8_t* _
 
 // Token tile: a tile costs a stage per 256 K whatever its width, so it should hold a whole segment;
 // mean + 2 sqrt(mean) covers nearly every one. Longer segments go to CTA pairs, where there is a
-// tile for each pair of SMs: 8 experts x 14336 x 4096 with 128 rows each took 55 us on pairs, 57 in
-// 128-token tiles, with 1024 rows 228 and 263; with 64 rows 51 and 49.
+// tile for each pair of SMs: 8 experts x 14336 x 4096 with 1024 rows each took 239 us on pairs and 266 in
+// 128-token tiles (in runs of 2 s, at the power limit, 275 and 308), with 128 rows 57 and 55, with 64 rows 54
+// and, in 64-token tiles, 50. The mean alone decides: with half of 16384 rows on one of 32 experts 2880 x 2880
+// took 112 us, with as many rows on each 107.
 // MOE_TOKEN_TILE=16|32|64|128 and MOE_GEMM_PAIRS=0|1 override the choice (tests, tuning).
 // Returns 16, 32, 64 or 128, or, where rows are in segment order or can be brought into it, kPairTile.
 int gemm_mxf4_tile(int G, int N, int M_alloc, bool pairs) {

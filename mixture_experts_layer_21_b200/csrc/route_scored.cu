@@ -294,8 +294,8 @@ struct RoutePlan {
 
 // One token, decided in fp32 where that decides. False where it cannot (infinite logits, more than 32
 // candidates within the error of each other); nothing is written then. What bounds it is the number
-// of instructions (with 256 experts in 8 groups 1046 a token took 27 us for 16384 tokens, 1260 30 us, 1600
-// 36; the weights in fp64 brought 27.0 to 28.7, with fp64 divisions 29.3).
+// of instructions (with 256 experts in 8 groups 1090 a token, 28.8 us for 16384 tokens; 1046 and 27.0 with
+// weights of fp32, 29.3 us with divisions in fp64; 1260 a token took 30 us, 1600 36).
 //
 // Error of the scores that rank. Sigmoid: the exponential's argument -l log2(e) rounds twice, 2^-23 |l|
 // relative to the exponential e, whose approximation is within 2^-22; e / (1 + e)^2 <= 1/4 and |l| e / (1 + e)^2
@@ -456,7 +456,8 @@ __device__ bool route_fast(const moe_route_args_t& a, const RoutePlan& plan, con
         if (top2 || a.bias) {  // the lowest kept score's lower end against the highest dropped one's upper end
             // a score's slack: of its s, up to two of them (softmax's sum to at most 1), and of the rounding of
             // its c and of their sum
-            const float e = __shfl_sync(0xffffffffu, (softmax ? 0x1p-17f + 0x1p-20f : 0x1p-19f) + 0x1p-22f * fminf(mag, FLT_MAX), src);
+            const float of_s = softmax ? 0x1p-17f + 0x1p-20f : 0x1p-19f;
+            const float e = __shfl_sync(0xffffffffu, of_s + 0x1p-22f * fminf(mag, FLT_MAX), src);
             const float lo = key_value(__reduce_min_sync(0xffffffffu, kept ? order_key(my - e) : 0xffffffffu));
             const float hi = key_value(__reduce_max_sync(0xffffffffu, is && !kept ? order_key(my + e) : 0u));
             if (!(lo > hi)) keep = groups64<BF16>(a, t, mx, c64);
