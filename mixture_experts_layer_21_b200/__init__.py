@@ -359,7 +359,7 @@ def moe_add_rmsnorm(x: torch.Tensor, weight=None, residual=None, eps: float = 1e
                     want_y: bool = True, deq: bool = False, out=None, stream=None):
     """r = x + residual; y = r / sqrt(mean(r^2) + eps) * weight; y optionally quantised to "mxfp8" or
     "mxfp4" rows. x bf16 or fp32 [T,H], residual bf16 [T,H], weight bf16 or fp32 [H] (rows of x and
-    residual in any stride).
+    residual in any stride of a multiple of 8 elements; tensors 16-byte aligned).
     ``out``: optional dict of caller-allocated outputs (any of residual, y, codes, scales, deq; the
     rows of residual and y may be strided, residual may be the input's own tensor); the others are
     allocated here. Returns a dict with those five, None where not asked for: ``residual`` (bf16
@@ -566,7 +566,7 @@ def moe_quantize_mxfp8(x: torch.Tensor, stream=None):
 
 
 def moe_quantize_mxfp4(x: torch.Tensor, deq: bool = False, out=None, stream=None):
-    """MXFP4 quantisation of rows (bf16 or fp32 [R,K], in any row stride): packed e2m1 codes [R,K/2],
+    """MXFP4 quantisation of rows (bf16 or fp32 [R,K], rows a multiple of 8 elements apart): packed e2m1 codes [R,K/2],
     e8m0 scales [R,K/32] and, with deq, the bf16 values they stand for [R,K] (else None). ``out``:
     optional dict of caller-allocated outputs (any of codes, scales, deq)."""
     R, K = x.shape

@@ -94,3 +94,22 @@ def test_outputs_are_memory_of_the_given_stream(name):
     assert len(got) == len(want)
     for a, b in zip(got, want):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_captured_with_the_stream_named(name):
+    """The capturing stream given as stream=: what the call allocates is the graph's."""
+    call = _calls()[name]
+    want = [t.clone() for t in _tensors(call(None))]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = _tensors(call(torch.cuda.current_stream()))
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    assert len(got) == len(want)
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
